@@ -6,13 +6,17 @@ Usage: ``python -m bit_codebook_quantized_amd.build`` (or ``__graft_entry__.buil
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libw4a8.so")
-SOURCES = ["w4a8_api.cpp", "rotate_quant.hip", "decode.hip", "gemv.hip", "gemm.hip", "quantize.hip", "regrid.hip", "grad.hip"]
+SOURCES = ["w4a8_api.cpp", "rotate_quant.hip", "decode.hip", "gemv.hip", "gemm.hip", "quantize.hip", "regrid.hip", "grad.hip",
+           "block_api.cpp", "rmsnorm.hip", "rope_kv8.hip", "kv8_attention.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
@@ -33,8 +37,6 @@ NO_SCRATCH = {"gemm.hip": "gemm_kernel"}
 def check_no_scratch(hipcc: str) -> None:
     """Compile each NO_SCRATCH source to gfx950 assembly and fail if a listed kernel
     uses private (scratch) memory."""
-    import re
-    import tempfile
     for src, kernel in NO_SCRATCH.items():
         with tempfile.TemporaryDirectory() as td:
             asm = os.path.join(td, "k.s")
@@ -56,11 +58,7 @@ def check_no_scratch(hipcc: str) -> None:
             raise RuntimeError(f"no {kernel} found in the assembly of {src}")
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every source into libw4a8.so next to this file; returns its path."""
-    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    tmp = LIB + ".tmp"
-    cmd = [hipcc, *HIPCC_FLAGS, "-o", tmp, *[os.path.join(CSRC, s) for s in SOURCES]]
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -70,7 +68,22 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
     if verbose and err.strip():
         print(err, file=sys.stderr)
-    check_no_scratch(hipcc)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every source (side by side) and link libw4a8.so next to this file; returns
+    its path."""
+    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+    tmp = LIB + ".tmp"
+    with tempfile.TemporaryDirectory() as td, ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+        objs = [os.path.join(td, s + ".o") for s in SOURCES]
+        flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+        jobs = [pool.submit(check_no_scratch, hipcc)]
+        jobs += [pool.submit(_run, [hipcc, *flags, "-c", "-o", o, os.path.join(CSRC, s)], verbose)
+                 for s, o in zip(SOURCES, objs)]
+        for j in jobs:
+            j.result()
+        _run([hipcc, "--offload-arch=gfx950", "-fPIC", "-shared", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB)
     return LIB
 
