@@ -107,17 +107,159 @@ __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// Page that holds tokens at .. of sequence b, or -1 (the token index is bounded first).
-__device__ __forceinline__ int64_t page_at(const AttArgs& a, const int32_t* table, int token, int len, int shift) {
-    const int t = token < len ? token : len - 1;
-    const int64_t p = table[t >> shift];
+// What the lanes of one query row share: maximum of the scores (log2 units), this lane's part
+// of the sums (l for lse, lo divides the result) and the largest value scale the row has seen.
+struct RowState {
+    float m, l, lo, vtop;
+};
+__device__ __forceinline__ RowState fresh_row() { return RowState{-__builtin_inff(), 0.0f, 0.0f, 0.0f}; }
+
+// Maximum and sum over the four lane groups of a row (lanes c, c + 16, c + 32, c + 48).
+__device__ __forceinline__ float group_max(float v) {
+    const uint32_t u = __float_as_uint(v);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t w = __float_as_uint(__builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+    const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    return __builtin_fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float group_sum(float v) {
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+}
+
+// What a lane knows of a tile: its 16 keys start at `key`, they are in one page.
+struct TileInfo {
+    float fk, fv;       // key scale times scale_log2, value scale
+    float vmax;         // largest value scale of the tile's pages (NaN ones left out)
+    int key;
+    bool present;       // the page exists
+};
+
+// One tile's scores (acc, before scaling) to weights pw (16 fp16 numbers, this lane's 16
+// tokens in order), the row's state, and the factor for its accumulated result.
+// all_seen: every row sees every key, and the value scales are positive numbers.
+__device__ __forceinline__ float softmax_tile(const f32x4 (&acc)[4], const TileInfo& t, bool all_seen, int begin, int end,
+                                              RowState& s, uint32_t (&pw)[8]) {
+    if (all_seen) {
+        float top = acc[0][0];
+#pragma unroll
+        for (int j = 1; j < 16; ++j) top = __builtin_fmaxf(top, acc[j >> 2][j & 3]);
+        top = group_max(top * t.fk);
+        const float mn = __builtin_fmaxf(s.m, top), vn = __builtin_fmaxf(s.vtop, t.vmax);
+        const float alpha = __builtin_amdgcn_exp2f(s.m - mn);
+        const float inv_top = __builtin_amdgcn_rcpf(vn), r = t.fv * inv_top;
+        const float alpha_o = s.vtop == vn ? alpha : alpha * (s.vtop * inv_top);
+        s.m = mn;
+        s.vtop = vn;
+        // 2^15 exp2(score - maximum) r, with r in the exponent; the sums are of weights without it
+        const float bias = W_EXP - mn + __builtin_amdgcn_logf(r);
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[j >> 1][2 * (j & 1)], t.fk, bias));
+            const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[j >> 1][2 * (j & 1) + 1], t.fk, bias));
+            sum += w0 + w1;
+            pw[j] = pack_f16(w0, w1);
+        }
+        sum *= __builtin_amdgcn_rcpf(r);
+        s.l = __builtin_fmaf(s.l, alpha, sum);
+        s.lo = __builtin_fmaf(s.lo, alpha, sum);
+        return alpha_o;
+    }
+    float x[16];
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const int key = t.key + j;
+        x[j] = key < end && key >= begin && t.present ? acc[j >> 2][j & 3] * t.fk : -__builtin_inff();
+        top = __builtin_fmaxf(top, x[j]);
+    }
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) any |= x[j] != -__builtin_inff();
+    const float vn = group_max(__builtin_fmaxf(s.vtop, any ? t.fv : 0.0f));
+    const float mn = __builtin_fmaxf(s.m, group_max(top));
+    const float ref = mn > -__builtin_inff() ? mn : 0.0f;          // a row that has seen no key yet
+    const float alpha = __builtin_amdgcn_exp2f(s.m - ref);
+    const float inv_top = vn > 0.0f ? 1.0f / vn : 0.0f, r = t.fv * inv_top;
+    const float alpha_o = s.vtop == vn ? alpha : alpha * (s.vtop * inv_top);
+    s.m = mn;
+    s.vtop = vn;
+    // Few keys may count here, so the sum that divides the result is taken of the weights as
+    // rounded: the rounding of a row with one key cancels, of few nearly.  And a masked
+    // weight times a NaN scale must not reach the product.
+    float sum = 0.0f, rounded = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        f16x2 w;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float p = __builtin_amdgcn_exp2f(x[2 * j + e] - ref + W_EXP);
+            sum += p;
+            w[e] = (_Float16)(p == 0.0f ? 0.0f : p * r);
+            rounded += (float)w[e];
+        }
+        pw[j] = __builtin_bit_cast(uint32_t, w);
+    }
+    s.l = __builtin_fmaf(s.l, alpha, sum);
+    s.lo = __builtin_fmaf(s.lo, alpha, r > 0.0f ? rounded / r : sum);
+    return alpha_o;
+}
+
+// The keys that rows row0 .. row0 + count - 1 of a sequence (count >= 1) see between them
+// (from low to top) and all of them (from high to common).
+struct Span {
+    int low, top, high, common;
+};
+__device__ __forceinline__ Span span_of(const AttArgs& a, const Seq& s, int row0, int count) {
+    const int first = s.pos0 + row0 / a.group, last = s.pos0 + (row0 + count - 1) / a.group;
+    Span p;
+    p.top = a.causal ? min(s.len, last + 1) : s.len;
+    p.common = a.causal ? min(s.len, first + 1) : s.len;
+    const int64_t lb = a.window > 0 ? (int64_t)first - a.window + 1 : 0, hb = a.window > 0 ? (int64_t)last - a.window + 1 : 0;
+    p.low = lb > 0 ? (int)(lb < s.len ? lb : s.len) : 0;
+    p.high = hb > 0 ? (int)(hb < s.len ? hb : s.len) : 0;
+    return p;
+}
+
+// One query row: its place in q and out, and the keys it sees.
+struct Row {
+    int token, head, begin, end;
+};
+__device__ __forceinline__ Row row_of(const AttArgs& a, const Seq& s, int kv_head, int row, int rows) {
+    const int r = row < rows ? row : rows - 1;
+    Row x;
+    x.token = r / a.group;
+    x.head = kv_head * a.group + r - x.token * a.group;
+    const int pos = s.pos0 + x.token;
+    x.end = a.causal && pos + 1 < s.len ? pos + 1 : s.len;
+    x.begin = a.window > 0 && pos - a.window + 1 > 0 ? (int)(pos - a.window + 1) : 0;
+    if (row >= rows) x.end = 0;
+    return x;
+}
+
+// Page of token `at` of a sequence (the index is bounded by its length first), -1 if it is
+// not a page of the cache.
+__device__ __forceinline__ int page_at(const AttArgs& a, const int32_t* table, int at, int len, int shift) {
+    const int p = table[(at < len ? at : len - 1) >> shift];
     return p >= 0 && p < a.c.pages ? p : -1;
 }
 
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l) - W_EXP) * 0.69314718055994531f;
+}
+
+// Few query rows: a block has 16 of them, its waves split the keys.  A wave loads its tile
+// straight into registers in the order of the matrix operands: the values of a tile while its
+// scores are made, the keys of the next one while its weights are used.
 template <int D>
 __global__ __launch_bounds__(64 * WAVES) void kv8_attention_kernel(AttArgs a) {
     constexpr int NK = D / 64;       // 16-byte key loads a lane and sub-tile
-    constexpr int NV = D / 16;       // value columns tiles
+    constexpr int NV = D / 16;       // value column tiles
     // the waves' results, joined at the end: O^T [wave][D][16 + 1], maxima and sums
     __shared__ float so[WAVES][D][ROWS + 1];
     __shared__ float sm[WAVES][ROWS], sl[WAVES][ROWS], slo[WAVES][ROWS];
@@ -129,38 +271,22 @@ __global__ __launch_bounds__(64 * WAVES) void kv8_attention_kernel(AttArgs a) {
     const int head = id % a.c.heads;
     id /= a.c.heads;
     const int64_t b = id / a.tiles;
-    const int tile_rows = id % a.tiles;
     const Seq s = seq_of(a, b);
-    const int rows = s.n * a.group;
-    const int row0 = tile_rows * ROWS;
+    const int rows = s.n * a.group, row0 = (id % a.tiles) * ROWS;
     if (row0 >= rows) return;
-    const int shift = 31 - __clz(a.c.page_tokens);
+    const int shift = 31 - __clz(a.c.page_tokens), in_page = a.c.page_tokens - 1;
     const int32_t* const table = a.c.table + b * a.c.table_stride;
 
-    // this lane's query row
-    const int row = row0 + c, rr = row < rows ? row : rows - 1;
-    const int token = rr / a.group, qh = head * a.group + rr % a.group;
-    const int pos = s.pos0 + token;
-    int end = a.causal && pos + 1 < s.len ? pos + 1 : s.len;          // keys below it are seen
-    int begin = a.window > 0 && pos - a.window + 1 > 0 ? (int)(pos - a.window + 1) : 0;
-    if (row >= rows) end = 0;
-    // what the block's rows see between them, and what all of them see
-    const int last_token = (min(row0 + ROWS, rows) - 1) / a.group, first_token = row0 / a.group;
-    const int top_end = a.causal ? min(s.len, s.pos0 + last_token + 1) : s.len;
-    const int low_end = a.causal ? min(s.len, s.pos0 + first_token + 1) : s.len;
-    const int64_t lb = a.window > 0 ? (int64_t)s.pos0 + first_token - a.window + 1 : 0;
-    const int64_t hb = a.window > 0 ? (int64_t)s.pos0 + last_token - a.window + 1 : 0;
-    const int low_begin = lb > 0 ? (int)lb : 0;
-    const int top_begin = hb > 0 ? (int)(hb < s.len ? hb : s.len) : 0;
+    const Row row = row_of(a, s, head, row0 + c, rows);
+    const Span span = span_of(a, s, row0, min(ROWS, rows - row0));
     const bool whole = row0 + ROWS <= rows;
-
     const int k_first = split * a.chunk;
-    const int k0 = max(k_first, low_begin / STEP * STEP);
-    const int k1 = split == a.splits - 1 ? top_end : min(top_end, k_first + a.chunk);
+    const int k0 = max(k_first, span.low / STEP * STEP) + wave * TILE;
+    const int k1 = split == a.splits - 1 ? span.top : min(span.top, k_first + a.chunk);
 
     bf16x8 qf[2 * NK];
     {
-        const uint16_t* src = a.q + (s.q0 + token) * a.q_stride + (int64_t)qh * D;
+        const uint16_t* src = a.q + (s.q0 + row.token) * a.q_stride + (int64_t)row.head * D;
 #pragma unroll
         for (int i = 0; i < NK; ++i)
 #pragma unroll
@@ -168,23 +294,45 @@ __global__ __launch_bounds__(64 * WAVES) void kv8_attention_kernel(AttArgs a) {
                 qf[2 * i + e] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(src + 64 * i + 16 * g + 8 * e));
     }
 
-    float m = -__builtin_inff(), l = 0.0f;
-    float lo = 0.0f;                 // the sum that divides the result (l is the one for lse)
-    float vtop = 0.0f;               // largest value scale that the row has seen
+    RowState st = fresh_row();
     f32x4 o[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) o[i] = f32x4{0, 0, 0, 0};
 
-    for (int kt = k0 + wave * TILE; kt < k1; kt += STEP) {
-        // keys: lane c loads rows of the page of tokens 16 (c / 4) .., values and scales: of 16 g ..
-        const int64_t pk = page_at(a, table, kt + 16 * (c >> 2), s.len, shift);
-        const int64_t pv = page_at(a, table, kt + 16 * g, s.len, shift);
-        const int in_page = (1 << shift) - 1;
-        const int8_t* kp = a.c.k + (((pk < 0 ? 0 : pk) * a.c.heads + head) << shift) * D +
-                           (int64_t)(((kt + 16 * (c >> 2)) & in_page) + (c & 3)) * D + 16 * g;
-        const int64_t vbase = (pv < 0 ? 0 : pv) * a.c.heads + head;
-        const int8_t* vp = a.c.v + ((vbase * D) << shift) + ((int64_t)c << shift) + ((kt + 16 * g) & in_page);
-        const float fk = a.c.k_scale[vbase] * a.scale_log2, fv = a.c.v_scale[vbase];
+    // lane (c, g): keys from row c of a sub-tile (tokens 16 (c / 4) + 4 j + c % 4), 16 codes of
+    // every 64; values of tokens 16 g .. 16 g + 15
+    uint4 kw[4 * NK];
+    // (page numbers are fetched a step before what they point at)
+    int pk = 0, pv = 0;
+    auto pages = [&](int kt) {
+        pk = page_at(a, table, kt + 16 * (c >> 2), s.len, shift);
+        pv = page_at(a, table, kt + 16 * g, s.len, shift);
+    };
+    auto load_keys = [&](int kt) {
+        const int8_t* kp = a.c.k + ((((int64_t)(pk < 0 ? 0 : pk) * a.c.heads + head) << shift) +
+                                    ((kt + 16 * (c >> 2)) & in_page) + (c & 3)) * D + 16 * g;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < NK; ++i) kw[j * NK + i] = *reinterpret_cast<const uint4*>(kp + 4 * j * D + 64 * i);
+    };
+    if (k0 < k1) {
+        pages(k0);
+        load_keys(k0);
+    }
+    for (int kt = k0; kt < k1; kt += STEP) {
+        const int64_t vpage = (int64_t)(pv < 0 ? 0 : pv) * a.c.heads + head;
+        const int8_t* vp = a.c.v + ((vpage * D) << shift) + ((int64_t)c << shift) + ((kt + 16 * g) & in_page);
+        TileInfo t;
+        t.fk = a.c.k_scale[vpage] * a.scale_log2;
+        t.fv = a.c.v_scale[vpage];
+        t.key = kt + 16 * g;
+        t.present = pv >= 0;
+        uint4 vw[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) vw[i] = *reinterpret_cast<const uint4*>(vp + ((int64_t)(16 * i) << shift));
+        const bool more = kt + STEP < k1;
+        if (more) pages(kt + STEP);
 
         f32x4 acc[4];
 #pragma unroll
@@ -192,94 +340,40 @@ __global__ __launch_bounds__(64 * WAVES) void kv8_attention_kernel(AttArgs a) {
             acc[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int i = 0; i < NK; ++i) {
-                const uint4 w = *reinterpret_cast<const uint4*>(kp + 4 * j * D + 64 * i);
+                const uint4 w = kw[j * NK + i];
                 acc[j] = mfma(widen(w.x, w.y), qf[2 * i], acc[j]);
                 acc[j] = mfma(widen(w.z, w.w), qf[2 * i + 1], acc[j]);
             }
         }
-        float x[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = acc[j >> 2][j & 3] * fk;
-        const bool masked = !whole || kt + TILE > low_end || kt < top_begin || __any(pv < 0);
-        if (masked) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int key = kt + 16 * g + j;
-                x[j] = key < end && key >= begin && pv >= 0 ? x[j] : -__builtin_inff();
-            }
-        }
-        float top = x[0];
-#pragma unroll
-        for (int j = 1; j < 16; ++j) top = __builtin_fmaxf(top, x[j]);
-        // the largest value scale of the pages that the row has seen (a NaN one is left to its
-        // own weights)
-        float vn = __builtin_fmaxf(vtop, masked && top == -__builtin_inff() ? 0.0f : fv);
-        top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-        top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-        vn = __builtin_fmaxf(vn, __shfl_xor(vn, 16));
-        vn = __builtin_fmaxf(vn, __shfl_xor(vn, 32));
-        const float mn = __builtin_fmaxf(m, top);
-        const float ref = mn > -__builtin_inff() ? mn : 0.0f;      // a row that has seen no key yet
-        const float alpha = __builtin_amdgcn_exp2f(m - ref);
-        const float inv_top = vn > 0.0f ? 1.0f / vn : 0.0f;
-        const float alpha_o = alpha * (vtop * inv_top), r = fv * inv_top;
-        m = mn;
-        vtop = vn;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) o[i] *= alpha_o;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = __builtin_amdgcn_exp2f(x[j] - ref + W_EXP);
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) sum += x[j];
-        l = l * alpha + sum;
+        if (more) load_keys(kt + STEP);
+        const bool odd = !whole || kt + TILE > span.common || kt < span.high || __any(!t.present || !(t.fv > 0.0f));
+        t.vmax = group_max(t.fv);
         uint32_t pw[8];
-        if (masked) {
-            // few keys may count here: their sum is taken of the weights as rounded, so that the
-            // roundings of a row with one key cancel, of few nearly; and a masked weight
-            // times a NaN scale must not reach the product
-            float rounded = 0.0f;
+        const float alpha = softmax_tile(acc, t, !odd, row.begin, row.end, st, pw);
+        if (__any(alpha != 1.0f)) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                f16x2 w;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    w[e] = (_Float16)(x[2 * j + e] == 0.0f ? 0.0f : x[2 * j + e] * r);
-                    rounded += (float)w[e];
-                }
-                pw[j] = __builtin_bit_cast(uint32_t, w);
-            }
-            lo = lo * alpha + (r > 0.0f ? rounded / r : sum);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                pw[j] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)(x[2 * j] * r), (_Float16)(x[2 * j + 1] * r)});
-            lo = lo * alpha + sum;
+            for (int i = 0; i < NV; ++i) o[i] *= alpha;
         }
         const f16x8 pf0 = __builtin_bit_cast(f16x8, make_uint4(pw[0], pw[1], pw[2], pw[3]));
         const f16x8 pf1 = __builtin_bit_cast(f16x8, make_uint4(pw[4], pw[5], pw[6], pw[7]));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const uint4 w = *reinterpret_cast<const uint4*>(vp + ((int64_t)(16 * i) << shift));
-            o[i] = mfma(widen_f16(w.x, w.y), pf0, o[i]);
-            o[i] = mfma(widen_f16(w.z, w.w), pf1, o[i]);
+            o[i] = mfma(widen_f16(vw[i].x, vw[i].y), pf0, o[i]);
+            o[i] = mfma(widen_f16(vw[i].z, vw[i].w), pf1, o[i]);
         }
     }
-    // a lane's l covers its own 16 keys of each tile
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    lo += __shfl_xor(lo, 16);
-    lo += __shfl_xor(lo, 32);
-
-    if (g == 0) { sm[wave][c] = m; sl[wave][c] = l; slo[wave][c] = lo; }
+    // a lane's sums cover its own 16 keys of each tile
+    st.l = group_sum(st.l);
+    st.lo = group_sum(st.lo);
+    if (g == 0) { sm[wave][c] = st.m; sl[wave][c] = st.l; slo[wave][c] = st.lo; }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) so[wave][16 * i + 4 * g + e][c] = o[i][e] * vtop;
+        for (int e = 0; e < 4; ++e) so[wave][16 * i + 4 * g + e][c] = o[i][e] * st.vtop;
     __syncthreads();
 
-    // join the waves: thread (r, d ..) takes row r
-    const int r = tid >> 4, d0 = tid & 15;     // 16 rows x 16 threads
+    // join the waves: 16 threads a row
+    const int r = tid >> 4, d0 = tid & 15;
     if (row0 + r >= rows) return;
     float mt = sm[0][r];
 #pragma unroll
@@ -293,7 +387,7 @@ __global__ __launch_bounds__(64 * WAVES) void kv8_attention_kernel(AttArgs a) {
         lot += slo[w][r] * f[w];
     }
     const int out_token = (row0 + r) / a.group, out_head = head * a.group + (row0 + r) % a.group;
-    const int64_t t = s.q0 + out_token;
+    const int64_t t = s.q0 + out_token, rid = t * a.q_heads + out_head;
     const float inv = lt == 0.0f ? 0.0f : 1.0f / lot;      // a row that sees no key: 0
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
@@ -302,22 +396,214 @@ __global__ __launch_bounds__(64 * WAVES) void kv8_attention_kernel(AttArgs a) {
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) v = __builtin_fmaf(so[w][d][r], f[w], v);
         if (a.splits == 1) a.out[t * a.out_stride + (int64_t)out_head * D + d] = f32_to_bf16(lt == 0.0f ? 0.0f : v * inv);
-        else a.part_o[((t * a.q_heads + out_head) * a.splits + split) * D + d] = v;
+        else a.part_o[(rid * a.splits + split) * D + d] = v;
     }
     if (d0 == 0) {
-        const int64_t id = t * a.q_heads + out_head;
         if (a.splits > 1) {
-            float* ml = a.part_ml + (id * a.splits + split) * 4;
+            float* ml = a.part_ml + (rid * a.splits + split) * 4;
             ml[0] = mt;
             ml[1] = lt;
             ml[2] = lot;
         } else if (a.lse) {
-            a.lse[id] = lt == 0.0f ? -__builtin_inff() : (mt + __builtin_log2f(lt) - W_EXP) * 0.69314718055994531f;
+            a.lse[rid] = lse_of(mt, lt);
         }
     }
 }
 
-// Joins the splits of one query row: 64 threads a row, D / 64 columns each.
+// Many query rows: a block has 256 of them, 32 a wave, and all its waves walk the same keys.
+// A tile is widened once a block on its way into LDS (two tiles in turn: the next one is
+// loaded while this one is used, one barrier a tile).  A key lies at row 16 j + 4 a + b of the
+// tile for key 16 a + 4 j + b, so that the 16 rows of a sub-tile follow each other; rows are
+// padded by 16 bytes, and 16 lanes reading 16 bytes each from consecutive rows meet no bank
+// twice.
+constexpr int PROMPT_ROWS = 128;     // from this many rows of a sequence on
+constexpr int P_WAVES = 8, P_QT = 2, P_ROWS = 16 * P_QT * P_WAVES;
+
+template <int D>
+__global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) {
+    constexpr int NS = D / 32, NV = D / 16;
+    constexpr int KS = D + 8, VS = TILE + 8;                // row strides, elements
+    constexpr int CHUNKS = TILE * D / 16;                   // 16-code pieces of a tile's keys, or values
+    __shared__ __attribute__((aligned(16))) uint16_t sk[2][TILE * KS];
+    __shared__ __attribute__((aligned(16))) uint16_t sv[2][D * VS];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
+    int id = blockIdx.x;                               // head fastest, then split, row tile, sequence
+    const int head = id % a.c.heads;
+    id /= a.c.heads;
+    const int split = id % a.splits;
+    id /= a.splits;
+    const int64_t b = id / a.tiles;
+    const Seq s = seq_of(a, b);
+    const int rows = s.n * a.group;
+    const int row0 = (a.tiles - 1 - id % a.tiles) * P_ROWS;     // the last rows see most: they start first
+    if (row0 >= rows) return;
+    const int shift = 31 - __clz(a.c.page_tokens), in_page = a.c.page_tokens - 1;
+    const int32_t* const table = a.c.table + b * a.c.table_stride;
+
+    const Span span = span_of(a, s, row0, min(P_ROWS, rows - row0));
+    const int k_first = split * a.chunk;
+    const int k0 = max(k_first, span.low / TILE * TILE);
+    const int k1 = split == a.splits - 1 ? span.top : min(span.top, k_first + a.chunk);
+
+    // this wave's rows
+    const int wrow0 = row0 + 16 * P_QT * wave;
+    const bool idle = wrow0 >= rows;
+    const Span wspan = span_of(a, s, idle ? row0 : wrow0, idle ? 1 : min(16 * P_QT, rows - wrow0));
+    const bool whole = wrow0 + 16 * P_QT <= rows;
+    Row row[P_QT];
+    bf16x8 qf[P_QT][NS];
+#pragma unroll
+    for (int t = 0; t < P_QT; ++t) {
+        row[t] = row_of(a, s, head, wrow0 + 16 * t + c, rows);
+        const uint16_t* src = a.q + (s.q0 + row[t].token) * a.q_stride + (int64_t)row[t].head * D + 8 * g;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) qf[t][i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(src + 32 * i));
+    }
+    RowState st[P_QT];
+    f32x4 o[P_QT][NV];
+#pragma unroll
+    for (int t = 0; t < P_QT; ++t) {
+        st[t] = fresh_row();
+#pragma unroll
+        for (int i = 0; i < NV; ++i) o[t][i] = f32x4{0, 0, 0, 0};
+    }
+
+    // This thread's piece of the staged tile.  D = 128: 16 codes of a key and 16 of a value column;
+    // D = 64: one of the two.
+    constexpr bool BOTH = CHUNKS == 64 * P_WAVES;
+    static_assert(BOTH || 2 * CHUNKS == 64 * P_WAVES, "a tile is one or two pieces a thread");
+    const bool does_k = BOTH || tid < CHUNKS, does_v = BOTH || tid >= CHUNKS;
+    const int piece = tid & (CHUNKS - 1);
+    const int skey = piece / (D / 16), sdim = 16 * (piece % (D / 16));          // key of the tile, first dim
+    const int sd = piece >> 2, stok = 16 * (piece & 3);                         // value column, first token
+    const int krow = 16 * ((skey >> 2) & 3) + 4 * (skey >> 4) + (skey & 3);
+    uint4 kw = make_uint4(0, 0, 0, 0), vw = make_uint4(0, 0, 0, 0);
+    // Page numbers are fetched a tile before what they point at: of the staged piece's keys and
+    // values, and (for the scales) of this lane's 16 tokens.
+    int pk = 0, pv = 0, ps = 0;
+    auto pages = [&](int kt) {
+        pk = page_at(a, table, kt + skey, s.len, shift);
+        pv = page_at(a, table, kt + stok, s.len, shift);
+        ps = page_at(a, table, kt + 16 * g, s.len, shift);
+    };
+    TileInfo next{};
+    auto load = [&](int kt) {
+        if (does_k)
+            kw = *reinterpret_cast<const uint4*>(
+                a.c.k + ((((int64_t)(pk < 0 ? 0 : pk) * a.c.heads + head) << shift) + ((kt + skey) & in_page)) * D + sdim);
+        if (does_v)
+            vw = *reinterpret_cast<const uint4*>(
+                a.c.v + ((((int64_t)(pv < 0 ? 0 : pv) * a.c.heads + head) * D + sd) << shift) + ((kt + stok) & in_page));
+        const int64_t page = (int64_t)(ps < 0 ? 0 : ps) * a.c.heads + head;
+        next.fk = a.c.k_scale[page];
+        next.fv = a.c.v_scale[page];
+        next.key = kt + 16 * g;
+        next.present = ps >= 0;
+    };
+    auto store = [&](int buf) {
+        if (does_k) {
+            uint4* dst = reinterpret_cast<uint4*>(&sk[buf][krow * KS + sdim]);
+            dst[0] = __builtin_bit_cast(uint4, widen(kw.x, kw.y));
+            dst[1] = __builtin_bit_cast(uint4, widen(kw.z, kw.w));
+        }
+        if (does_v) {
+            uint4* dst = reinterpret_cast<uint4*>(&sv[buf][sd * VS + stok]);
+            dst[0] = __builtin_bit_cast(uint4, widen_f16(vw.x, vw.y));
+            dst[1] = __builtin_bit_cast(uint4, widen_f16(vw.z, vw.w));
+        }
+    };
+
+    if (k0 < k1) {
+        pages(k0);
+        load(k0);
+        pages(k0 + TILE);
+        store(0);
+    }
+    int buf = 0;
+    for (int kt = k0; kt < k1; kt += TILE, buf ^= 1) {
+        __syncthreads();
+        const bool more = kt + TILE < k1;
+        TileInfo info = next;
+        info.fk *= a.scale_log2;
+        if (more) {
+            load(kt + TILE);
+            pages(kt + 2 * TILE);
+        }
+        if (!idle && kt < wspan.top && kt + TILE > wspan.low) {
+            f32x4 acc[P_QT][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int t = 0; t < P_QT; ++t) acc[t][j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    const bf16x8 k = __builtin_bit_cast(
+                        bf16x8, *reinterpret_cast<const uint4*>(&sk[buf][(16 * j + c) * KS + 32 * i + 8 * g]));
+#pragma unroll
+                    for (int t = 0; t < P_QT; ++t) acc[t][j] = mfma(k, qf[t][i], acc[t][j]);
+                }
+            }
+            const bool odd =
+                !whole || kt + TILE > wspan.common || kt < wspan.high || __any(!info.present || !(info.fv > 0.0f));
+            info.vmax = group_max(info.fv);
+            f16x8 pf[P_QT][2];
+#pragma unroll
+            for (int t = 0; t < P_QT; ++t) {
+                uint32_t pw[8];
+                const float alpha = softmax_tile(acc[t], info, !odd, row[t].begin, row[t].end, st[t], pw);
+                if (__any(alpha != 1.0f)) {
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) o[t][i] *= alpha;
+                }
+                pf[t][0] = __builtin_bit_cast(f16x8, make_uint4(pw[0], pw[1], pw[2], pw[3]));
+                pf[t][1] = __builtin_bit_cast(f16x8, make_uint4(pw[4], pw[5], pw[6], pw[7]));
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const f16x8 v = __builtin_bit_cast(
+                        f16x8, *reinterpret_cast<const uint4*>(&sv[buf][(16 * i + c) * VS + 16 * g + 8 * e]));
+#pragma unroll
+                    for (int t = 0; t < P_QT; ++t) o[t][i] = mfma(v, pf[t][e], o[t][i]);
+                }
+        }
+        if (more) store(buf ^ 1);
+    }
+
+    // lane (c, g) holds columns 16 i + 4 g .. + 3 of its rows
+#pragma unroll
+    for (int t = 0; t < P_QT; ++t) {
+        const float l = group_sum(st[t].l), lo = group_sum(st[t].lo);
+        if (wrow0 + 16 * t + c >= rows) continue;
+        const int64_t tok = s.q0 + row[t].token, rid = tok * a.q_heads + row[t].head;
+        if (a.splits == 1) {
+            const float inv = l == 0.0f ? 0.0f : st[t].vtop / lo;
+            uint16_t* dst = a.out + tok * a.out_stride + (int64_t)row[t].head * D + 4 * g;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const f32x4 v = o[t][i] * inv;
+                *reinterpret_cast<uint2*>(dst + 16 * i) =
+                    l == 0.0f ? make_uint2(0, 0) : make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
+            }
+            if (a.lse && g == 0) a.lse[rid] = lse_of(st[t].m, l);
+        } else {
+            float* dst = a.part_o + (rid * a.splits + split) * D + 4 * g;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) *reinterpret_cast<f32x4*>(dst + 16 * i) = o[t][i] * st[t].vtop;
+            if (g == 0) {
+                float* ml = a.part_ml + (rid * a.splits + split) * 4;
+                ml[0] = st[t].m;
+                ml[1] = l;
+                ml[2] = lo;
+            }
+        }
+    }
+}
+
+// Joins the splits of one query row: a wave a row, lane i holds split i's maximum and sums
+// (at most 64 splits).
 template <int D>
 __global__ __launch_bounds__(64) void kv8_join_kernel(AttArgs a) {
     int bid = blockIdx.x;
@@ -330,38 +616,55 @@ __global__ __launch_bounds__(64) void kv8_join_kernel(AttArgs a) {
     const int64_t t = s.q0 + row / a.group;
     const int qh = head * a.group + row % a.group;
     const int64_t id = t * a.q_heads + qh;
-    const float* ml = a.part_ml + id * a.splits * 4;
     const float* po = a.part_o + id * a.splits * D;
-    float mt = -__builtin_inff();
-    for (int i = 0; i < a.splits; ++i) mt = __builtin_fmaxf(mt, ml[4 * i]);
+    float4 ml = make_float4(-__builtin_inff(), 0.0f, 0.0f, 0.0f);
+    if (lane < a.splits) ml = *reinterpret_cast<const float4*>(a.part_ml + (id * a.splits + lane) * 4);
+    float mt = ml.x;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) mt = __builtin_fmaxf(mt, __shfl_xor(mt, o));
     const float ref = mt > -__builtin_inff() ? mt : 0.0f;
-    float lt = 0.0f, lot = 0.0f, v[D / 64];
+    const float f = __builtin_amdgcn_exp2f(ml.x - ref);
+    float lt = ml.y * f, lot = ml.z * f;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        lt += __shfl_xor(lt, o);
+        lot += __shfl_xor(lot, o);
+    }
+    float v[D / 64];
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) v[j] = 0.0f;
+#pragma unroll 4
     for (int i = 0; i < a.splits; ++i) {
-        const float f = __builtin_amdgcn_exp2f(ml[4 * i] - ref);
-        lt += ml[4 * i + 1] * f;
-        lot += ml[4 * i + 2] * f;
+        const float w = __shfl(f, i);
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) v[j] = __builtin_fmaf(po[(int64_t)i * D + lane + 64 * j], f, v[j]);
+        for (int j = 0; j < D / 64; ++j) v[j] = __builtin_fmaf(po[(int64_t)i * D + lane + 64 * j], w, v[j]);
     }
     const float inv = 1.0f / lot;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j)
         a.out[t * a.out_stride + (int64_t)qh * D + lane + 64 * j] = f32_to_bf16(lt == 0.0f ? 0.0f : v[j] * inv);
-    if (a.lse && lane == 0) a.lse[id] = lt == 0.0f ? -__builtin_inff() : (mt + __builtin_log2f(lt) - W_EXP) * 0.69314718055994531f;
+    if (a.lse && lane == 0) a.lse[id] = lse_of(mt, lt);
 }
 
-int64_t row_tiles(int64_t max_new, int group) { return (max_new * group + ROWS - 1) / ROWS; }
+// Rows of a block: 256 where a sequence has that many, else 16 (the keys are then split over
+// the waves).
+bool is_prompt(int64_t max_new, int group) { return max_new * group >= PROMPT_ROWS; }
+int64_t row_tiles(int64_t max_new, int group) {
+    const int r = is_prompt(max_new, group) ? P_ROWS : ROWS;
+    return (max_new * group + r - 1) / r;
+}
 
 }  // namespace
 
-// How the context is divided: enough splits for about 8 blocks a CU, none shorter than two
-// steps, at most 64.
+// How the context is divided: few rows, for eight blocks a CU (uneven lengths even out), and at
+// least one tile a wave; many, for a block a CU, and at least eight tiles; at most 64.
 int attention_splits(int64_t B, int64_t max_new, int64_t max_kv, int q_heads, int kv_heads) {
-    const int64_t base = std::max<int64_t>(1, B * kv_heads * row_tiles(max_new, q_heads / kv_heads));
-    const int64_t want = (2048 + base - 1) / base, most = std::max<int64_t>(1, max_kv / (2 * STEP));
-    return (int)std::min<int64_t>(64, std::min(want, most));
+    const int group = q_heads / kv_heads;
+    const bool prompt = is_prompt(max_new, group);
+    const int64_t base = std::max<int64_t>(1, B * kv_heads * row_tiles(max_new, group));
+    const int64_t want = prompt ? 256 / base : (4096 + base - 1) / base;
+    const int64_t most = max_kv / (prompt ? 8 * TILE : STEP);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(64, std::min(want, most)));
 }
 
 // Blocks of the main launch and of the join.
@@ -391,8 +694,13 @@ hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const 
     a.part_ml = workspace + T * q_heads * a.splits * c.head_dim;
     a.tiles = (int)row_tiles(max_new, a.group);
     const dim3 grid((unsigned)attention_blocks(B, max_new, max_kv, q_heads, c.heads));
-    if (c.head_dim == 64) hipLaunchKernelGGL(kv8_attention_kernel<64>, grid, dim3(64 * WAVES), 0, stream, a);
-    else hipLaunchKernelGGL(kv8_attention_kernel<128>, grid, dim3(64 * WAVES), 0, stream, a);
+    if (is_prompt(max_new, a.group)) {
+        if (c.head_dim == 64) hipLaunchKernelGGL(kv8_prompt_kernel<64>, grid, dim3(64 * P_WAVES), 0, stream, a);
+        else hipLaunchKernelGGL(kv8_prompt_kernel<128>, grid, dim3(64 * P_WAVES), 0, stream, a);
+    } else {
+        if (c.head_dim == 64) hipLaunchKernelGGL(kv8_attention_kernel<64>, grid, dim3(64 * WAVES), 0, stream, a);
+        else hipLaunchKernelGGL(kv8_attention_kernel<128>, grid, dim3(64 * WAVES), 0, stream, a);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     const dim3 jgrid((unsigned)attention_join_blocks(B, max_new, q_heads));
