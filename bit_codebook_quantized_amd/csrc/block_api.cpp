@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../include/w4a8_block.h"
+#include "kv8_plan.hpp"
 
 namespace w4a8 {
 hipError_t launch_rmsnorm_quant(const void* x, const void* residual, int stream_f32, const float* weight, int64_t M,
@@ -22,9 +23,6 @@ hipError_t launch_append(const w4a8_kv8& c, const int32_t* ctx_len, const int32_
                          int64_t max_new, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                          const void* q, int q_heads, int64_t q_stride, const w4a8_rope* rope, void* q_out,
                          int64_t out_stride, hipStream_t stream);
-int attention_splits(int64_t B, int64_t max_new, int64_t max_kv, int q_heads, int kv_heads);
-int64_t attention_blocks(int64_t B, int64_t max_new, int64_t max_kv, int q_heads, int kv_heads);
-int64_t attention_join_blocks(int64_t B, int64_t max_new, int q_heads);
 hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const w4a8_kv8& c, const int32_t* kv_len,
                             const int32_t* q_start, int64_t B, int64_t T, int64_t max_new, int64_t max_kv, float scale,
                             int causal, int64_t window, void* out, int64_t out_stride, float* lse, float* workspace,
@@ -101,6 +99,11 @@ int check_batch(int64_t B, int64_t T, int64_t max_new) {
 
 // No sequence has more new tokens than there are rows.
 int64_t bounded_new(int64_t T, int64_t max_new) { return max_new < T ? max_new : T; }
+
+// The query rows of a batch are within a launch's blocks.
+bool fits(int64_t B, int64_t max_new, int64_t q_heads) {
+    return B <= MAX_BLOCKS && max_new * q_heads <= MAX_BLOCKS && B * max_new * q_heads <= MAX_BLOCKS;
+}
 
 }  // namespace
 
@@ -205,8 +208,10 @@ int64_t kv8_attention_workspace(int64_t B, int64_t T, int64_t max_new, int64_t m
     if (check_batch(B, T, max_new) || max_kv < 0 || max_kv > MAX_TOKENS || kv_heads < 1 || q_heads < kv_heads ||
         q_heads % kv_heads != 0 || q_heads > MAX_HEADS || (head_dim != 64 && head_dim != 128))
         return 0;
-    const int64_t splits = w4a8::attention_splits(B, bounded_new(T, max_new), max_kv, q_heads, kv_heads);
-    return splits > 1 ? T * q_heads * splits * (head_dim + 4) * (int64_t)sizeof(float) : 0;
+    max_new = bounded_new(T, max_new);
+    if (B == 0 || max_new == 0 || !fits(B, max_new, q_heads)) return 0;
+    return w4a8::attention_workspace(w4a8::attention_plan(B, max_new, max_kv, q_heads, kv_heads, head_dim), T, q_heads,
+                                     head_dim) * (int64_t)sizeof(float);
 }
 
 int kv8_attention(const void* q, int32_t q_heads, int64_t q_stride, const w4a8_kv8* cache, const int32_t* kv_len,
@@ -224,15 +229,15 @@ int kv8_attention(const void* q, int32_t q_heads, int64_t q_stride, const w4a8_k
     if (q_heads % cache->heads != 0) return W4A8_ERR_SHAPE;
     if (T > 0 && (!q || !out)) return W4A8_ERR_INVALID_ARG;
     if (B > 0 && (!kv_len || !q_start)) return W4A8_ERR_INVALID_ARG;
-    const int64_t need = kv8_attention_workspace(B, T, max_new, max_kv, q_heads, cache->heads, cache->head_dim);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return W4A8_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(kv_len, 4) || !aligned(q_start, 4) || !aligned(lse, 4) ||
         !aligned(workspace, 16))
         return W4A8_ERR_ALIGN;
+    const int64_t need = kv8_attention_workspace(B, T, max_new, max_kv, q_heads, cache->heads, cache->head_dim);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return W4A8_ERR_INVALID_ARG;
     max_new = bounded_new(T, max_new);
     if (B == 0 || max_new == 0) return W4A8_OK;
-    if (B > MAX_BLOCKS || max_new * q_heads > MAX_BLOCKS || B * max_new * q_heads > MAX_BLOCKS ||
-        w4a8::attention_blocks(B, max_new, max_kv, q_heads, cache->heads) > MAX_BLOCKS)
+    if (!fits(B, max_new, q_heads) ||
+        w4a8::attention_plan(B, max_new, max_kv, q_heads, cache->heads, cache->head_dim).blocks > MAX_BLOCKS)
         return W4A8_ERR_SHAPE;
     return launched(w4a8::launch_attention(q, q_heads, q_stride, *cache, kv_len, q_start, B, T, max_new, max_kv, scale,
                                            causal, window, out, out_stride, lse, static_cast<float*>(workspace),

@@ -23,6 +23,7 @@
 #include <stdint.h>
 
 #include "../../include/w4a8_block.h"
+#include "kv8_plan.hpp"
 #include "w4a8_device.hpp"
 
 namespace w4a8 {
@@ -38,6 +39,7 @@ constexpr int ROWS = 16;             // query rows of a block
 constexpr int WAVES = 4;             // waves of a block: they share the rows and split the keys
 constexpr int STEP = TILE * WAVES;   // keys of a block's step
 constexpr float W_EXP = 15.0f;       // weights are kept times 2^15
+constexpr int64_t DEAL_BLOCKS = 512;  // few rows: blocks that share the steps
 
 struct AttArgs {
     w4a8_kv8 c;
@@ -47,11 +49,13 @@ struct AttArgs {
     const int32_t* kv_len;
     const int32_t* q_start;
     int64_t q_stride, out_stride, T, max_new, window;
-    float* part_o;        // [T * q_heads, splits, head_dim], of this split's own maximum
-    float* part_ml;       // [T * q_heads, splits, 4]: maximum (log2 units), the two sums, unused
+    float* part_o;        // parts: [part row, head_dim], relative to the part's own maximum;
+    float* part_ml;       // [part row, 4]: that maximum (log2 units), the two sums, unused.
+                          // Part rows: many query rows, T * q_heads * splits; few, blocks * 2 * 16
+    int4* part_job;       // few rows, [blocks]: item (-1: nothing to join), head, last block, first slot
     float scale_log2;     // scale * log2(e)
     int q_heads, group, causal;
-    int tiles;            // row tiles of a sequence with max_new tokens
+    int tiles, items;     // row tiles of a sequence with max_new tokens; of all sequences
     int splits, chunk;    // keys of a split (a multiple of STEP); the last one takes the rest
 };
 
@@ -253,160 +257,340 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l) - W_EXP) * 0.69314718055994531f;
 }
 
-// Few query rows: a block has 16 of them, its waves split the keys.  A wave loads its tile
-// straight into registers in the order of the matrix operands: the values of a tile while its
-// scores are made, the keys of the next one while its weights are used.
+// Few query rows.  The work is a list of steps of 256 keys: for every sequence, row tile (16
+// rows) and head, the steps that its rows see.  The list is dealt to the blocks in equal
+// contiguous shares, whatever the sequences' lengths are, so a block holds pieces of a few
+// (row tile, head) pairs; a piece that is not all of one leaves its part in the workspace
+// (a block has at most two such pieces: one that starts its share, one that ends it), and
+// kv8_join_kernel adds the parts up.  Rows that see no key still have one (empty) step.
+struct Item {            // one sequence's row tile
+    Seq s;
+    Span span;
+    int row0, rows, steps;    // steps of one head, 0 if the tile has no rows
+};
+__device__ __forceinline__ Item item_of(const AttArgs& a, int index) {
+    Item x;
+    x.s = seq_of(a, index / a.tiles);
+    x.rows = x.s.n * a.group;
+    x.row0 = (index % a.tiles) * ROWS;
+    x.steps = 0;
+    if (x.row0 < x.rows) {
+        x.span = span_of(a, x.s, x.row0, min(ROWS, x.rows - x.row0));
+        const int n = (x.span.top + STEP - 1) / STEP - x.span.low / STEP;
+        x.steps = n > 0 ? n : 1;
+    }
+    return x;
+}
+
+__device__ __forceinline__ int64_t wave_prefix(int64_t v, int lane) {      // inclusive
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int64_t u = __shfl_up(v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// A value that every lane holds, into scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    return (int64_t)((uint64_t)(uint32_t)uniform((int)v) | (uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32);
+}
+
+// Steps of all items (whole wave).
+__device__ __forceinline__ int64_t total_steps(const AttArgs& a, int lane) {
+    int64_t sum = 0;
+    for (int i = 0; i < a.items; i += 64) {
+        int64_t v = i + lane < a.items ? (int64_t)item_of(a, i + lane).steps * a.c.heads : 0;
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+        sum += v;
+    }
+    return uniform(sum);
+}
+
+// n / d for 0 <= n < 2^52, d > 0, the same in every lane: through fp64, put right by one where the quotient rounded up.
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+    const int64_t q = (int64_t)((double)n / (double)d);
+    return uniform(q * d > n ? q - 1 : q);
+}
+
+// The list dealt to `blocks` blocks (at most one for each step): block i's share starts at
+// from(i); the first `rest` shares are one step longer than the others.
+struct Shares {
+    int64_t blocks, each, rest;
+    __device__ __forceinline__ int64_t from(int64_t i) const { return i * each + (i < rest ? i : rest); }
+    __device__ __forceinline__ int64_t block_of(int64_t at) const {
+        const int64_t longer = rest * (each + 1);
+        return at < longer ? quotient(at, each + 1) : rest + quotient(at - longer, each);
+    }
+};
+__device__ __forceinline__ Shares shares_of(int64_t total, int64_t blocks) {
+    Shares s;
+    s.blocks = blocks < total ? blocks : total;
+    s.each = s.blocks > 0 ? quotient(total, s.blocks) : 0;
+    s.rest = total - s.each * s.blocks;
+    return s;
+}
+
+// The item that holds position `at` of the list (at < total), and where it starts.
+__device__ __forceinline__ int item_at(const AttArgs& a, int64_t at, int lane, int64_t& before) {
+    int64_t sum = 0;
+    for (int i = 0; i < a.items; i += 64) {
+        const int64_t v = i + lane < a.items ? (int64_t)item_of(a, i + lane).steps * a.c.heads : 0;
+        const int64_t p = sum + wave_prefix(v, lane);
+        const uint64_t past = __ballot(p > at);
+        if (past != 0) {
+            const int first = __ffsll((unsigned long long)past) - 1;
+            before = uniform(__shfl(p - v, first));
+            return uniform(i + first);
+        }
+        sum = __shfl(p, 63);
+    }
+    before = sum;
+    return a.items;
+}
+
+// A wave loads its tile straight into registers in the order of the matrix operands: the
+// values of a tile while its scores are made, the keys of the next one while its weights are
+// used.  The four waves take the step's four tiles and are joined through LDS.
 template <int D>
-__global__ __launch_bounds__(64 * WAVES) void kv8_attention_kernel(AttArgs a) {
+__global__ __launch_bounds__(64 * WAVES, 2) void kv8_attention_kernel(AttArgs a) {
     constexpr int NK = D / 64;       // 16-byte key loads a lane and sub-tile
     constexpr int NV = D / 16;       // value column tiles
-    // the waves' results, joined at the end: O^T [wave][D][16 + 1], maxima and sums
+    // the waves' results: O^T [wave][D][16 + 1], maxima and sums
     __shared__ float so[WAVES][D][ROWS + 1];
     __shared__ float sm[WAVES][ROWS], sl[WAVES][ROWS], slo[WAVES][ROWS];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
-    int id = blockIdx.x;                               // split fastest, then head, row tile, sequence
-    const int split = id % a.splits;
-    id /= a.splits;
-    const int head = id % a.c.heads;
-    id /= a.c.heads;
-    const int64_t b = id / a.tiles;
-    const Seq s = seq_of(a, b);
-    const int rows = s.n * a.group, row0 = (id % a.tiles) * ROWS;
-    if (row0 >= rows) return;
+    const Shares deal = shares_of(total_steps(a, lane), gridDim.x);
+    if (tid == 0) a.part_job[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    if (blockIdx.x >= deal.blocks) return;
+    const int64_t from = deal.from(blockIdx.x), to = deal.from(blockIdx.x + 1);
+    int64_t before;
+    int index = item_at(a, from, lane, before);
     const int shift = 31 - __clz(a.c.page_tokens), in_page = a.c.page_tokens - 1;
-    const int32_t* const table = a.c.table + b * a.c.table_stride;
 
-    const Row row = row_of(a, s, head, row0 + c, rows);
-    const Span span = span_of(a, s, row0, min(ROWS, rows - row0));
-    const bool whole = row0 + ROWS <= rows;
-    const int k_first = split * a.chunk;
-    const int k0 = max(k_first, span.low / STEP * STEP) + wave * TILE;
-    const int k1 = split == a.splits - 1 ? span.top : min(span.top, k_first + a.chunk);
+    for (int64_t at = from; at < to && index < a.items;) {
+        const Item x = item_of(a, index);
+        const int64_t size = (int64_t)x.steps * a.c.heads;
+        if (at >= before + size) {         // this item is done (or has no rows)
+            before += size;
+            ++index;
+            continue;
+        }
+        const int head = (int)quotient(at - before, x.steps), step = (int)((at - before) - (int64_t)head * x.steps);
+        const int steps = (int)(to - at < x.steps - step ? to - at : x.steps - step);
+        const Seq& s = x.s;
+        const Span& span = x.span;
+        const int rows = x.rows, row0 = x.row0;
+        const int32_t* const table = a.c.table + (int64_t)(index / a.tiles) * a.c.table_stride;
+        const Row row = row_of(a, s, head, row0 + c, rows);
+        const bool whole = row0 + ROWS <= rows;
+        const int first = (span.low / STEP + step) * STEP;
+        const int k0 = first + wave * TILE, k1 = min(span.top, first + steps * STEP);
 
-    bf16x8 qf[2 * NK];
-    {
-        const uint16_t* src = a.q + (s.q0 + row.token) * a.q_stride + (int64_t)row.head * D;
+        bf16x8 qf[2 * NK];
+        {
+            const uint16_t* src = a.q + (s.q0 + row.token) * a.q_stride + (int64_t)row.head * D;
 #pragma unroll
-        for (int i = 0; i < NK; ++i)
+            for (int i = 0; i < NK; ++i)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                qf[2 * i + e] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(src + 64 * i + 16 * g + 8 * e));
-    }
+                for (int e = 0; e < 2; ++e)
+                    qf[2 * i + e] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(src + 64 * i + 16 * g + 8 * e));
+        }
+        RowState st = fresh_row();
+        f32x4 o[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) o[i] = f32x4{0, 0, 0, 0};
 
-    RowState st = fresh_row();
-    f32x4 o[NV];
+        // lane (c, g): keys from row c of a sub-tile (tokens 16 (c / 4) + 4 j + c % 4), 16 codes
+        // of every 64; values of tokens 16 g .. 16 g + 15.  Page numbers are fetched a step
+        // before what they point at.
+        uint4 kw[4 * NK];
+        int pk = 0, pv = 0;
+        auto pages = [&](int kt) {
+            pk = page_at(a, table, kt + 16 * (c >> 2), s.len, shift);
+            pv = page_at(a, table, kt + 16 * g, s.len, shift);
+        };
+        auto load_keys = [&](int kt) {
+            const int8_t* kp = a.c.k + ((((int64_t)(pk < 0 ? 0 : pk) * a.c.heads + head) << shift) +
+                                        ((kt + 16 * (c >> 2)) & in_page) + (c & 3)) * D + 16 * g;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) o[i] = f32x4{0, 0, 0, 0};
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < NK; ++i) kw[j * NK + i] = *reinterpret_cast<const uint4*>(kp + 4 * j * D + 64 * i);
+        };
+        if (k0 < k1) {
+            pages(k0);
+            load_keys(k0);
+        }
+        for (int kt = k0; kt < k1; kt += STEP) {
+            const int64_t vpage = (int64_t)(pv < 0 ? 0 : pv) * a.c.heads + head;
+            const int8_t* vp = a.c.v + ((vpage * D) << shift) + ((int64_t)c << shift) + ((kt + 16 * g) & in_page);
+            TileInfo t;
+            t.fk = a.c.k_scale[vpage] * a.scale_log2;
+            t.fv = a.c.v_scale[vpage];
+            t.key = kt + 16 * g;
+            t.present = pv >= 0;
+            uint4 vw[NV];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) vw[i] = *reinterpret_cast<const uint4*>(vp + ((int64_t)(16 * i) << shift));
+            const bool more = kt + STEP < k1;
+            if (more) pages(kt + STEP);
 
-    // lane (c, g): keys from row c of a sub-tile (tokens 16 (c / 4) + 4 j + c % 4), 16 codes of
-    // every 64; values of tokens 16 g .. 16 g + 15
-    uint4 kw[4 * NK];
-    // (page numbers are fetched a step before what they point at)
-    int pk = 0, pv = 0;
-    auto pages = [&](int kt) {
-        pk = page_at(a, table, kt + 16 * (c >> 2), s.len, shift);
-        pv = page_at(a, table, kt + 16 * g, s.len, shift);
-    };
-    auto load_keys = [&](int kt) {
-        const int8_t* kp = a.c.k + ((((int64_t)(pk < 0 ? 0 : pk) * a.c.heads + head) << shift) +
-                                    ((kt + 16 * (c >> 2)) & in_page) + (c & 3)) * D + 16 * g;
+            f32x4 acc[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j) {
+                acc[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < NK; ++i) kw[j * NK + i] = *reinterpret_cast<const uint4*>(kp + 4 * j * D + 64 * i);
-    };
-    if (k0 < k1) {
-        pages(k0);
-        load_keys(k0);
-    }
-    for (int kt = k0; kt < k1; kt += STEP) {
-        const int64_t vpage = (int64_t)(pv < 0 ? 0 : pv) * a.c.heads + head;
-        const int8_t* vp = a.c.v + ((vpage * D) << shift) + ((int64_t)c << shift) + ((kt + 16 * g) & in_page);
-        TileInfo t;
-        t.fk = a.c.k_scale[vpage] * a.scale_log2;
-        t.fv = a.c.v_scale[vpage];
-        t.key = kt + 16 * g;
-        t.present = pv >= 0;
-        uint4 vw[NV];
+                for (int i = 0; i < NK; ++i) {
+                    const uint4 w = kw[j * NK + i];
+                    acc[j] = mfma(widen(w.x, w.y), qf[2 * i], acc[j]);
+                    acc[j] = mfma(widen(w.z, w.w), qf[2 * i + 1], acc[j]);
+                }
+            }
+            if (more) load_keys(kt + STEP);
+            const bool odd = !whole || kt + TILE > span.common || kt < span.high || __any(!t.present || !(t.fv > 0.0f));
+            t.vmax = group_max(t.fv);
+            uint32_t pw[8];
+            const float alpha = softmax_tile(acc, t, !odd, row.begin, row.end, st, pw);
+            if (__any(alpha != 1.0f)) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) vw[i] = *reinterpret_cast<const uint4*>(vp + ((int64_t)(16 * i) << shift));
-        const bool more = kt + STEP < k1;
-        if (more) pages(kt + STEP);
-
-        f32x4 acc[4];
+                for (int i = 0; i < NV; ++i) o[i] *= alpha;
+            }
+            const f16x8 pf0 = __builtin_bit_cast(f16x8, make_uint4(pw[0], pw[1], pw[2], pw[3]));
+            const f16x8 pf1 = __builtin_bit_cast(f16x8, make_uint4(pw[4], pw[5], pw[6], pw[7]));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            acc[j] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int i = 0; i < NK; ++i) {
-                const uint4 w = kw[j * NK + i];
-                acc[j] = mfma(widen(w.x, w.y), qf[2 * i], acc[j]);
-                acc[j] = mfma(widen(w.z, w.w), qf[2 * i + 1], acc[j]);
+            for (int i = 0; i < NV; ++i) {
+                o[i] = mfma(widen_f16(vw[i].x, vw[i].y), pf0, o[i]);
+                o[i] = mfma(widen_f16(vw[i].z, vw[i].w), pf1, o[i]);
             }
         }
-        if (more) load_keys(kt + STEP);
-        const bool odd = !whole || kt + TILE > span.common || kt < span.high || __any(!t.present || !(t.fv > 0.0f));
-        t.vmax = group_max(t.fv);
-        uint32_t pw[8];
-        const float alpha = softmax_tile(acc, t, !odd, row.begin, row.end, st, pw);
-        if (__any(alpha != 1.0f)) {
+        // a lane's sums cover its own 16 keys of each tile
+        st.l = group_sum(st.l);
+        st.lo = group_sum(st.lo);
+        if (g == 0) { sm[wave][c] = st.m; sl[wave][c] = st.l; slo[wave][c] = st.lo; }
 #pragma unroll
-            for (int i = 0; i < NV; ++i) o[i] *= alpha;
-        }
-        const f16x8 pf0 = __builtin_bit_cast(f16x8, make_uint4(pw[0], pw[1], pw[2], pw[3]));
-        const f16x8 pf1 = __builtin_bit_cast(f16x8, make_uint4(pw[4], pw[5], pw[6], pw[7]));
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            o[i] = mfma(widen_f16(vw[i].x, vw[i].y), pf0, o[i]);
-            o[i] = mfma(widen_f16(vw[i].z, vw[i].w), pf1, o[i]);
-        }
-    }
-    // a lane's sums cover its own 16 keys of each tile
-    st.l = group_sum(st.l);
-    st.lo = group_sum(st.lo);
-    if (g == 0) { sm[wave][c] = st.m; sl[wave][c] = st.l; slo[wave][c] = st.lo; }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) so[wave][16 * i + 4 * g + e][c] = o[i][e] * st.vtop;
-    __syncthreads();
+            for (int e = 0; e < 4; ++e) so[wave][16 * i + 4 * g + e][c] = o[i][e] * st.vtop;
+        __syncthreads();
 
-    // join the waves: 16 threads a row
-    const int r = tid >> 4, d0 = tid & 15;
-    if (row0 + r >= rows) return;
-    float mt = sm[0][r];
+        // join the waves: 16 threads a row
+        const int r = tid >> 4, d0 = tid & 15;
+        if (row0 + r < rows) {
+            float mt = sm[0][r];
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) mt = __builtin_fmaxf(mt, sm[w][r]);
-    const float ref = mt > -__builtin_inff() ? mt : 0.0f;
-    float f[WAVES], lt = 0.0f, lot = 0.0f;
+            for (int w = 1; w < WAVES; ++w) mt = __builtin_fmaxf(mt, sm[w][r]);
+            const float ref = mt > -__builtin_inff() ? mt : 0.0f;
+            float f[WAVES], lt = 0.0f, lot = 0.0f;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-        f[w] = __builtin_amdgcn_exp2f(sm[w][r] - ref);
-        lt += sl[w][r] * f[w];
-        lot += slo[w][r] * f[w];
-    }
-    const int out_token = (row0 + r) / a.group, out_head = head * a.group + (row0 + r) % a.group;
-    const int64_t t = s.q0 + out_token, rid = t * a.q_heads + out_head;
-    const float inv = lt == 0.0f ? 0.0f : 1.0f / lot;      // a row that sees no key: 0
+            for (int w = 0; w < WAVES; ++w) {
+                f[w] = __builtin_amdgcn_exp2f(sm[w][r] - ref);
+                lt += sl[w][r] * f[w];
+                lot += slo[w][r] * f[w];
+            }
+            const bool final = steps == x.steps;
+            const int out_token = (row0 + r) / a.group, out_head = head * a.group + (row0 + r) % a.group;
+            const int64_t t = s.q0 + out_token, rid = t * a.q_heads + out_head;
+            const int64_t slot = (2 * (int64_t)blockIdx.x + (at == from ? 0 : 1)) * ROWS + r;
+            const float inv = lt == 0.0f ? 0.0f : 1.0f / lot;      // a row that sees no key: 0
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-        const int d = d0 + 16 * i;
-        float v = 0.0f;
+            for (int i = 0; i < D / 16; ++i) {
+                const int d = d0 + 16 * i;
+                float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) v = __builtin_fmaf(so[w][d][r], f[w], v);
-        if (a.splits == 1) a.out[t * a.out_stride + (int64_t)out_head * D + d] = f32_to_bf16(lt == 0.0f ? 0.0f : v * inv);
-        else a.part_o[(rid * a.splits + split) * D + d] = v;
-    }
-    if (d0 == 0) {
-        if (a.splits > 1) {
-            float* ml = a.part_ml + (rid * a.splits + split) * 4;
-            ml[0] = mt;
-            ml[1] = lt;
-            ml[2] = lot;
-        } else if (a.lse) {
-            a.lse[rid] = lse_of(mt, lt);
+                for (int w = 0; w < WAVES; ++w) v = __builtin_fmaf(so[w][d][r], f[w], v);
+                if (final) a.out[t * a.out_stride + (int64_t)out_head * D + d] = f32_to_bf16(lt == 0.0f ? 0.0f : v * inv);
+                else a.part_o[slot * D + d] = v;
+            }
+            if (d0 == 0) {
+                if (!final) *reinterpret_cast<float4*>(a.part_ml + slot * 4) = make_float4(mt, lt, lot, 0.0f);
+                else if (a.lse) a.lse[rid] = lse_of(mt, lt);
+            }
         }
+        // The piece that begins a row tile and head, and does not end it, names who joins the
+        // parts: this block's number and the last block that has one.
+        if (tid == 0 && step == 0 && steps < x.steps)
+            a.part_job[blockIdx.x] = make_int4(index, head, (int)deal.block_of(at + x.steps - 1), at == from ? 0 : 1);
+        __syncthreads();       // before the next piece's results
+        at += steps;
+    }
+}
+
+// Joins the parts of the row tile and head that block blockIdx.x of the main launch began: the
+// waves take parts in turn with a running maximum, then join through LDS.  A lane has 4 columns
+// of every 64 / (D / 4)-th row.
+template <int D>
+__global__ __launch_bounds__(64 * WAVES) void kv8_join_steps_kernel(AttArgs a) {
+    constexpr int LANES = D / 4, AT_ONCE = 64 / LANES, NR = ROWS / AT_ONCE;
+    __shared__ __attribute__((aligned(16))) float so[WAVES][ROWS][D];
+    __shared__ float sm[WAVES][ROWS], sl[WAVES][ROWS], slo[WAVES][ROWS];
+    const int4 job = a.part_job[blockIdx.x];
+    if (job.x < 0) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int sub = lane / LANES, col = 4 * (lane % LANES);
+    const Item x = item_of(a, job.x);
+    const int count = min(ROWS, x.rows - x.row0);
+    const int first = blockIdx.x, last = job.z;
+
+    f32x4 v[NR];
+    float m[NR], l[NR], lo[NR];
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+        v[j] = f32x4{0, 0, 0, 0};
+        m[j] = -__builtin_inff();
+        l[j] = lo[j] = 0.0f;
+    }
+    for (int i = first + wave; i <= last; i += WAVES) {
+        const int64_t slot = (2 * (int64_t)i + (i == first ? job.w : 0)) * ROWS;
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            const int r = AT_ONCE * j + sub;
+            if (r >= count) continue;
+            const float4 ml = *reinterpret_cast<const float4*>(a.part_ml + (slot + r) * 4);
+            const f32x4 p = *reinterpret_cast<const f32x4*>(a.part_o + (slot + r) * D + col);
+            const float mn = __builtin_fmaxf(m[j], ml.x), ref = mn > -__builtin_inff() ? mn : 0.0f;
+            const float f0 = __builtin_amdgcn_exp2f(m[j] - ref), f1 = __builtin_amdgcn_exp2f(ml.x - ref);
+            m[j] = mn;
+            l[j] = l[j] * f0 + ml.y * f1;
+            lo[j] = lo[j] * f0 + ml.z * f1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[j][e] = __builtin_fmaf(p[e], f1, v[j][e] * f0);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+        const int r = AT_ONCE * j + sub;
+        if (r >= count) continue;
+        *reinterpret_cast<f32x4*>(&so[wave][r][col]) = v[j];
+        if (col == 0) { sm[wave][r] = m[j]; sl[wave][r] = l[j]; slo[wave][r] = lo[j]; }
+    }
+    __syncthreads();
+    for (int i = tid; i < count * LANES; i += 64 * WAVES) {
+        const int r = i / LANES, d = 4 * (i % LANES);
+        float mt = sm[0][r];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) mt = __builtin_fmaxf(mt, sm[w][r]);
+        const float ref = mt > -__builtin_inff() ? mt : 0.0f;
+        float lt = 0.0f, lot = 0.0f;
+        f32x4 y = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const float f = __builtin_amdgcn_exp2f(sm[w][r] - ref);
+            lt += sl[w][r] * f;
+            lot += slo[w][r] * f;
+            const f32x4 p = *reinterpret_cast<const f32x4*>(&so[w][r][d]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(p[e], f, y[e]);
+        }
+        const int64_t t = x.s.q0 + (x.row0 + r) / a.group;
+        const int qh = job.y * a.group + (x.row0 + r) % a.group;
+        const float inv = 1.0f / lot;
+        *reinterpret_cast<uint2*>(a.out + t * a.out_stride + (int64_t)qh * D + d) =
+            lt == 0.0f ? make_uint2(0, 0) : make_uint2(f32x2_to_bf16x2(y[0] * inv, y[1] * inv), f32x2_to_bf16x2(y[2] * inv, y[3] * inv));
+        if (a.lse && d == 0) a.lse[t * a.q_heads + qh] = lse_of(mt, lt);
     }
 }
 
@@ -656,23 +840,32 @@ int64_t row_tiles(int64_t max_new, int group) {
 
 }  // namespace
 
-// How the context is divided: few rows, for eight blocks a CU (uneven lengths even out), and at
-// least one tile a wave; many, for a block a CU, and at least eight tiles; at most 64.
-int attention_splits(int64_t B, int64_t max_new, int64_t max_kv, int q_heads, int kv_heads) {
+// Blocks of a launch, and for many rows the splits of the context.  Few rows: two blocks a CU,
+// as many as fit at once, or one for each step if there are fewer.  Many: enough splits for a
+// block a CU, none below eight tiles.
+AttentionPlan attention_plan(int64_t B, int64_t max_new, int64_t max_kv, int q_heads, int kv_heads, int head_dim) {
     const int group = q_heads / kv_heads;
-    const bool prompt = is_prompt(max_new, group);
-    const int64_t base = std::max<int64_t>(1, B * kv_heads * row_tiles(max_new, group));
-    const int64_t want = prompt ? 256 / base : (4096 + base - 1) / base;
-    const int64_t most = max_kv / (prompt ? 8 * TILE : STEP);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(64, std::min(want, most)));
+    AttentionPlan p{};
+    p.prompt = is_prompt(max_new, group);
+    const int64_t base = B * kv_heads * row_tiles(max_new, group);
+    if (p.prompt) {
+        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(64, std::min(256 / std::max<int64_t>(1, base), max_kv / (8 * TILE))));
+        p.blocks = base * p.splits;
+        p.join_blocks = p.splits > 1 ? B * max_new * q_heads : 0;
+        p.part_rows = p.splits > 1 ? p.splits : 0;          // times the rows of q
+        return p;
+    }
+    p.splits = 1;
+    p.blocks = std::min<int64_t>(DEAL_BLOCKS, base * std::max<int64_t>(1, (max_kv + STEP - 1) / STEP));
+    p.join_blocks = p.blocks;
+    p.part_rows = p.blocks * 2 * ROWS;
+    return p;
 }
 
-// Blocks of the main launch and of the join.
-int64_t attention_blocks(int64_t B, int64_t max_new, int64_t max_kv, int q_heads, int kv_heads) {
-    return B * row_tiles(max_new, q_heads / kv_heads) * kv_heads *
-           attention_splits(B, max_new, max_kv, q_heads, kv_heads);
+// Floats of workspace.
+int64_t attention_workspace(const AttentionPlan& p, int64_t T, int q_heads, int head_dim) {
+    return (p.prompt ? T * q_heads * p.part_rows : p.part_rows) * (head_dim + 4) + (p.prompt ? 0 : 4 * p.blocks);
 }
-int64_t attention_join_blocks(int64_t B, int64_t max_new, int q_heads) { return B * max_new * q_heads; }
 
 hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const w4a8_kv8& c, const int32_t* kv_len,
                             const int32_t* q_start, int64_t B, int64_t T, int64_t max_new, int64_t max_kv, float scale,
@@ -688,24 +881,30 @@ hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const 
     a.q_stride = q_stride; a.out_stride = out_stride; a.T = T; a.max_new = max_new; a.window = window;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.q_heads = q_heads; a.group = q_heads / c.heads; a.causal = causal;
-    a.splits = attention_splits(B, max_new, max_kv, q_heads, c.heads);
+    const AttentionPlan p = attention_plan(B, max_new, max_kv, q_heads, c.heads, c.head_dim);
+    a.splits = p.splits;
     a.chunk = (int)((max_kv + a.splits - 1) / a.splits + STEP - 1) / STEP * STEP;
     a.part_o = workspace;
-    a.part_ml = workspace + T * q_heads * a.splits * c.head_dim;
+    a.part_ml = workspace + (p.prompt ? T * q_heads * p.part_rows : p.part_rows) * c.head_dim;
+    a.part_job = reinterpret_cast<int4*>(a.part_ml + p.part_rows * 4);     // few rows only
     a.tiles = (int)row_tiles(max_new, a.group);
-    const dim3 grid((unsigned)attention_blocks(B, max_new, max_kv, q_heads, c.heads));
-    if (is_prompt(max_new, a.group)) {
+    a.items = (int)(B * a.tiles);
+    const dim3 grid((unsigned)p.blocks), join((unsigned)p.join_blocks);
+    if (p.prompt) {
         if (c.head_dim == 64) hipLaunchKernelGGL(kv8_prompt_kernel<64>, grid, dim3(64 * P_WAVES), 0, stream, a);
         else hipLaunchKernelGGL(kv8_prompt_kernel<128>, grid, dim3(64 * P_WAVES), 0, stream, a);
-    } else {
-        if (c.head_dim == 64) hipLaunchKernelGGL(kv8_attention_kernel<64>, grid, dim3(64 * WAVES), 0, stream, a);
-        else hipLaunchKernelGGL(kv8_attention_kernel<128>, grid, dim3(64 * WAVES), 0, stream, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || p.join_blocks == 0) return e;
+        if (c.head_dim == 64) hipLaunchKernelGGL(kv8_join_kernel<64>, join, dim3(64), 0, stream, a);
+        else hipLaunchKernelGGL(kv8_join_kernel<128>, join, dim3(64), 0, stream, a);
+        return hipGetLastError();
     }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.splits == 1) return e;
-    const dim3 jgrid((unsigned)attention_join_blocks(B, max_new, q_heads));
-    if (c.head_dim == 64) hipLaunchKernelGGL(kv8_join_kernel<64>, jgrid, dim3(64), 0, stream, a);
-    else hipLaunchKernelGGL(kv8_join_kernel<128>, jgrid, dim3(64), 0, stream, a);
+    if (c.head_dim == 64) hipLaunchKernelGGL(kv8_attention_kernel<64>, grid, dim3(64 * WAVES), 0, stream, a);
+    else hipLaunchKernelGGL(kv8_attention_kernel<128>, grid, dim3(64 * WAVES), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (c.head_dim == 64) hipLaunchKernelGGL(kv8_join_steps_kernel<64>, join, dim3(64 * WAVES), 0, stream, a);
+    else hipLaunchKernelGGL(kv8_join_steps_kernel<128>, join, dim3(64 * WAVES), 0, stream, a);
     return hipGetLastError();
 }
 
