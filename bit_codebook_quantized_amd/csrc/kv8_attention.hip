@@ -19,6 +19,7 @@
 // The rows of a tile are (token, query head) pairs of one cache head, so a group of query
 // heads shares the keys that it reads.
 #include <algorithm>
+#include <type_traits>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -58,6 +59,12 @@ struct AttArgs {
     int tiles, items;     // row tiles of a sequence with max_new tokens; of all sequences
     int splits, chunk;    // keys of a split (a multiple of STEP); the last one takes the rest
 };
+
+// A value that every lane holds, into scalar registers.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    return (int64_t)((uint64_t)(uint32_t)uniform((int)v) | (uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32);
+}
 
 // The query rows of sequence b: how many new tokens, where they start, how long the cache is.
 struct Seq {
@@ -111,12 +118,13 @@ __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-// What the lanes of one query row share: maximum of the scores (log2 units), this lane's part
-// of the sums (l for lse, lo divides the result) and the largest value scale the row has seen.
+// The state of one query row, the same in its four lanes: maximum of the scores (log2 units),
+// the sums (l for lse, lo divides the result), and log2 of the largest value scale that the row
+// has seen.
 struct RowState {
-    float m, l, lo, vtop;
+    float m, l, lo, lv;
 };
-__device__ __forceinline__ RowState fresh_row() { return RowState{-__builtin_inff(), 0.0f, 0.0f, 0.0f}; }
+__device__ __forceinline__ RowState fresh_row() { return RowState{-__builtin_inff(), 0.0f, 0.0f, -__builtin_inff()}; }
 
 // Maximum and sum over the four lane groups of a row (lanes c, c + 16, c + 32, c + 48).
 __device__ __forceinline__ float group_max(float v) {
@@ -127,8 +135,11 @@ __device__ __forceinline__ float group_max(float v) {
     return __builtin_fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float group_sum(float v) {
-    v += __shfl_xor(v, 16);
-    return v + __shfl_xor(v, 32);
+    const uint32_t u = __float_as_uint(v);
+    const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t w = __float_as_uint(__uint_as_float(a[0]) + __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
@@ -137,66 +148,107 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 
 // What a lane knows of a tile: its 16 keys start at `key`, they are in one page.
 struct TileInfo {
-    float fk, fv;       // key scale times scale_log2, value scale
-    float vmax;         // largest value scale of the tile's pages (NaN ones left out)
+    float fk, fv;         // key scale times scale_log2, value scale
+    float lfv, lvmax;     // log2 of fv, and the largest of the tile's pages (NaN left out)
     int key;
-    bool present;       // the page exists
+    bool present;         // the page exists
 };
+// With ONE_PAGE the whole tile is in one page.
+template <bool ONE_PAGE>
+__device__ __forceinline__ TileInfo tile_info(float k_scale, float v_scale, float scale_log2, int key, bool present) {
+    TileInfo t;
+    t.fk = k_scale * scale_log2;
+    t.fv = v_scale;
+    t.lfv = __builtin_amdgcn_logf(v_scale);
+    t.lvmax = ONE_PAGE ? t.lfv : group_max(t.lfv);
+    t.key = key;
+    t.present = present;
+    return t;
+}
+// Whether the tile needs no care: every page exists and has a positive value scale.
+__device__ __forceinline__ bool plain_tile(const TileInfo& t) { return __all(t.present && t.lfv > -__builtin_inff()); }
 
-// One tile's scores (acc, before scaling) to weights pw (16 fp16 numbers, this lane's 16
-// tokens in order), the row's state, and the factor for its accumulated result.
-// all_seen: every row sees every key, and the value scales are positive numbers.
-__device__ __forceinline__ float softmax_tile(const f32x4 (&acc)[4], const TileInfo& t, bool all_seen, int begin, int end,
-                                              RowState& s, uint32_t (&pw)[8]) {
-    if (all_seen) {
-        float top = acc[0][0];
+struct Weights {
+    f16x8 lo, hi;         // of this lane's tokens 0 .. 7 and 8 .. 15
+};
+__device__ __forceinline__ Weights weights_of(const uint32_t (&w)[8]) {
+    return Weights{__builtin_bit_cast(f16x8, make_uint4(w[0], w[1], w[2], w[3])),
+                   __builtin_bit_cast(f16x8, make_uint4(w[4], w[5], w[6], w[7]))};
+}
+
+// One tile's scores (acc, before scaling) to weights, the row's state, and the factor for its
+// accumulated result; here where every row sees every key of a plain tile.  The value scale
+// goes into the exponent, and (with one page) the sum of the weights is a matrix product with
+// ones, both because the vector ALU is what this loop runs out of first.
+template <bool ONE_PAGE>
+__device__ __forceinline__ float softmax_plain(const f32x4 (&acc)[4], const TileInfo& t, bool want_lse, RowState& s,
+                                               Weights& w) {
+    float top = acc[0][0];
 #pragma unroll
-        for (int j = 1; j < 16; ++j) top = __builtin_fmaxf(top, acc[j >> 2][j & 3]);
-        top = group_max(top * t.fk);
-        const float mn = __builtin_fmaxf(s.m, top), vn = __builtin_fmaxf(s.vtop, t.vmax);
-        const float alpha = __builtin_amdgcn_exp2f(s.m - mn);
-        const float inv_top = __builtin_amdgcn_rcpf(vn), r = t.fv * inv_top;
-        const float alpha_o = s.vtop == vn ? alpha : alpha * (s.vtop * inv_top);
-        s.m = mn;
-        s.vtop = vn;
-        // 2^15 exp2(score - maximum) r, with r in the exponent; the sums are of weights without it
-        const float bias = W_EXP - mn + __builtin_amdgcn_logf(r);
-        float sum = 0.0f;
+    for (int j = 1; j < 16; ++j) top = __builtin_fmaxf(top, acc[j >> 2][j & 3]);
+    const float mn = __builtin_fmaxf(s.m, group_max(top * t.fk)), lvn = __builtin_fmaxf(s.lv, t.lvmax);
+    const float r = t.lfv - lvn;
+    const float alpha = __builtin_amdgcn_exp2f(s.m - mn), alpha_o = __builtin_amdgcn_exp2f((s.m - mn) + (s.lv - lvn));
+    const float bias = (W_EXP - mn) + r;
+    float p[16];
+    uint32_t pw[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[j >> 1][2 * (j & 1)], t.fk, bias));
-            const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[j >> 1][2 * (j & 1) + 1], t.fk, bias));
-            sum += w0 + w1;
-            pw[j] = pack_f16(w0, w1);
-        }
-        sum *= __builtin_amdgcn_rcpf(r);
-        s.l = __builtin_fmaf(s.l, alpha, sum);
-        s.lo = __builtin_fmaf(s.lo, alpha, sum);
-        return alpha_o;
+    for (int j = 0; j < 16; ++j) p[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[j >> 2][j & 3], t.fk, bias));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) pw[j] = pack_f16(p[2 * j], p[2 * j + 1]);
+    w = weights_of(pw);
+    // the sum of the weights without the value scale, as rounded; lse takes them as they were
+    float sum = 0.0f;
+    if constexpr (ONE_PAGE) {
+        const f16x8 ones = {1, 1, 1, 1, 1, 1, 1, 1};
+        f32x4 all = {0, 0, 0, 0};
+        all = mfma(ones, w.lo, all);
+        all = mfma(ones, w.hi, all);
+        sum = all[0] * __builtin_amdgcn_exp2f(-r);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            sum = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, pw[j]), f16x2{1, 1}, sum, false);
+        sum = group_sum(sum * __builtin_amdgcn_exp2f(-r));
     }
+    s.m = mn;
+    s.lv = lvn;
+    s.lo = __builtin_fmaf(s.lo, alpha, sum);
+    if (want_lse) {
+        sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum += p[j];
+        sum = group_sum(sum * __builtin_amdgcn_exp2f(-r));
+    }
+    s.l = __builtin_fmaf(s.l, alpha, sum);
+    return alpha_o;
+}
+
+// The same for any tile.  Few keys may count in one that is partly masked, so the sum that
+// divides the result is taken of the weights as rounded (the rounding of a row with one key
+// cancels, of few nearly), and the one for lse before; and a masked weight times a NaN scale
+// must not reach the product.
+__device__ __forceinline__ float softmax_any(const f32x4 (&acc)[4], const TileInfo& t, int begin, int end, RowState& s,
+                                             Weights& wt) {
     float x[16];
     float top = -__builtin_inff();
+    bool any = false;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
         const int key = t.key + j;
-        x[j] = key < end && key >= begin && t.present ? acc[j >> 2][j & 3] * t.fk : -__builtin_inff();
+        const bool seen = key < end && key >= begin && t.present;
+        x[j] = seen ? acc[j >> 2][j & 3] * t.fk : -__builtin_inff();
         top = __builtin_fmaxf(top, x[j]);
+        any |= seen;
     }
-    bool any = false;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) any |= x[j] != -__builtin_inff();
-    const float vn = group_max(__builtin_fmaxf(s.vtop, any ? t.fv : 0.0f));
+    const float lvn = group_max(__builtin_fmaxf(s.lv, any ? t.lfv : -__builtin_inff()));
     const float mn = __builtin_fmaxf(s.m, group_max(top));
     const float ref = mn > -__builtin_inff() ? mn : 0.0f;          // a row that has seen no key yet
     const float alpha = __builtin_amdgcn_exp2f(s.m - ref);
-    const float inv_top = vn > 0.0f ? 1.0f / vn : 0.0f, r = t.fv * inv_top;
-    const float alpha_o = s.vtop == vn ? alpha : alpha * (s.vtop * inv_top);
-    s.m = mn;
-    s.vtop = vn;
-    // Few keys may count here, so the sum that divides the result is taken of the weights as
-    // rounded: the rounding of a row with one key cancels, of few nearly.  And a masked
-    // weight times a NaN scale must not reach the product.
+    const float alpha_o = s.lv == lvn ? alpha : alpha * __builtin_amdgcn_exp2f(s.lv - lvn);
+    const float r = t.lfv > -__builtin_inff() ? __builtin_amdgcn_exp2f(t.lfv - lvn) : t.fv;
     float sum = 0.0f, rounded = 0.0f;
+    uint32_t pw[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         f16x2 w;
@@ -209,8 +261,11 @@ __device__ __forceinline__ float softmax_tile(const f32x4 (&acc)[4], const TileI
         }
         pw[j] = __builtin_bit_cast(uint32_t, w);
     }
-    s.l = __builtin_fmaf(s.l, alpha, sum);
-    s.lo = __builtin_fmaf(s.lo, alpha, r > 0.0f ? rounded / r : sum);
+    wt = weights_of(pw);
+    s.m = mn;
+    s.lv = lvn;
+    s.l = __builtin_fmaf(s.l, alpha, group_sum(sum));
+    s.lo = __builtin_fmaf(s.lo, alpha, group_sum(any && r > 0.0f ? rounded / r : sum));
     return alpha_o;
 }
 
@@ -291,12 +346,6 @@ __device__ __forceinline__ int64_t wave_prefix(int64_t v, int lane) {      // in
     return v;
 }
 
-// A value that every lane holds, into scalar registers.
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-    return (int64_t)((uint64_t)(uint32_t)uniform((int)v) | (uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32);
-}
-
 // Steps of all items (whole wave).
 __device__ __forceinline__ int64_t total_steps(const AttArgs& a, int lane) {
     int64_t sum = 0;
@@ -354,7 +403,7 @@ __device__ __forceinline__ int item_at(const AttArgs& a, int64_t at, int lane, i
 // A wave loads its tile straight into registers in the order of the matrix operands: the
 // values of a tile while its scores are made, the keys of the next one while its weights are
 // used.  The four waves take the step's four tiles and are joined through LDS.
-template <int D>
+template <int D, bool ONE_PAGE>
 __global__ __launch_bounds__(64 * WAVES, 2) void kv8_attention_kernel(AttArgs a) {
     constexpr int NK = D / 64;       // 16-byte key loads a lane and sub-tile
     constexpr int NV = D / 16;       // value column tiles
@@ -362,7 +411,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv8_attention_kernel(AttArgs a)
     __shared__ float so[WAVES][D][ROWS + 1];
     __shared__ float sm[WAVES][ROWS], sl[WAVES][ROWS], slo[WAVES][ROWS];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), c = lane & 15, g = lane >> 4;
     const Shares deal = shares_of(total_steps(a, lane), gridDim.x);
     if (tid == 0) a.part_job[blockIdx.x] = make_int4(-1, 0, 0, 0);
     if (blockIdx.x >= deal.blocks) return;
@@ -370,6 +419,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv8_attention_kernel(AttArgs a)
     int64_t before;
     int index = item_at(a, from, lane, before);
     const int shift = 31 - __clz(a.c.page_tokens), in_page = a.c.page_tokens - 1;
+    const bool want_lse = a.lse != nullptr;
 
     for (int64_t at = from; at < to && index < a.items;) {
         const Item x = item_of(a, index);
@@ -410,8 +460,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv8_attention_kernel(AttArgs a)
         uint4 kw[4 * NK];
         int pk = 0, pv = 0;
         auto pages = [&](int kt) {
-            pk = page_at(a, table, kt + 16 * (c >> 2), s.len, shift);
-            pv = page_at(a, table, kt + 16 * g, s.len, shift);
+            if constexpr (ONE_PAGE) {
+                pk = pv = uniform(page_at(a, table, uniform(kt), s.len, shift));
+            } else {
+                pk = page_at(a, table, kt + 16 * (c >> 2), s.len, shift);
+                pv = page_at(a, table, kt + 16 * g, s.len, shift);
+            }
         };
         auto load_keys = [&](int kt) {
             const int8_t* kp = a.c.k + ((((int64_t)(pk < 0 ? 0 : pk) * a.c.heads + head) << shift) +
@@ -428,11 +482,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv8_attention_kernel(AttArgs a)
         for (int kt = k0; kt < k1; kt += STEP) {
             const int64_t vpage = (int64_t)(pv < 0 ? 0 : pv) * a.c.heads + head;
             const int8_t* vp = a.c.v + ((vpage * D) << shift) + ((int64_t)c << shift) + ((kt + 16 * g) & in_page);
-            TileInfo t;
-            t.fk = a.c.k_scale[vpage] * a.scale_log2;
-            t.fv = a.c.v_scale[vpage];
-            t.key = kt + 16 * g;
-            t.present = pv >= 0;
+            const float ks = a.c.k_scale[vpage], vs = a.c.v_scale[vpage];
+            const bool present = pv >= 0;
             uint4 vw[NV];
 #pragma unroll
             for (int i = 0; i < NV; ++i) vw[i] = *reinterpret_cast<const uint4*>(vp + ((int64_t)(16 * i) << shift));
@@ -451,30 +502,26 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv8_attention_kernel(AttArgs a)
                 }
             }
             if (more) load_keys(kt + STEP);
-            const bool odd = !whole || kt + TILE > span.common || kt < span.high || __any(!t.present || !(t.fv > 0.0f));
-            t.vmax = group_max(t.fv);
-            uint32_t pw[8];
-            const float alpha = softmax_tile(acc, t, !odd, row.begin, row.end, st, pw);
+            const TileInfo t = tile_info<ONE_PAGE>(ks, vs, a.scale_log2, kt + 16 * g, present);
+            const bool plain = whole && kt + TILE <= span.common && kt >= span.high && plain_tile(t);
+            Weights w;
+            const float alpha = plain ? softmax_plain<ONE_PAGE>(acc, t, want_lse, st, w) : softmax_any(acc, t, row.begin, row.end, st, w);
             if (__any(alpha != 1.0f)) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) o[i] *= alpha;
             }
-            const f16x8 pf0 = __builtin_bit_cast(f16x8, make_uint4(pw[0], pw[1], pw[2], pw[3]));
-            const f16x8 pf1 = __builtin_bit_cast(f16x8, make_uint4(pw[4], pw[5], pw[6], pw[7]));
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                o[i] = mfma(widen_f16(vw[i].x, vw[i].y), pf0, o[i]);
-                o[i] = mfma(widen_f16(vw[i].z, vw[i].w), pf1, o[i]);
+                o[i] = mfma(widen_f16(vw[i].x, vw[i].y), w.lo, o[i]);
+                o[i] = mfma(widen_f16(vw[i].z, vw[i].w), w.hi, o[i]);
             }
         }
-        // a lane's sums cover its own 16 keys of each tile
-        st.l = group_sum(st.l);
-        st.lo = group_sum(st.lo);
+        const float vtop = __builtin_amdgcn_exp2f(st.lv);
         if (g == 0) { sm[wave][c] = st.m; sl[wave][c] = st.l; slo[wave][c] = st.lo; }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) so[wave][16 * i + 4 * g + e][c] = o[i][e] * st.vtop;
+            for (int e = 0; e < 4; ++e) so[wave][16 * i + 4 * g + e][c] = o[i][e] * vtop;
         __syncthreads();
 
         // join the waves: 16 threads a row
@@ -603,7 +650,7 @@ __global__ __launch_bounds__(64 * WAVES) void kv8_join_steps_kernel(AttArgs a) {
 constexpr int PROMPT_ROWS = 128;     // from this many rows of a sequence on
 constexpr int P_WAVES = 8, P_QT = 2, P_ROWS = 16 * P_QT * P_WAVES;
 
-template <int D>
+template <int D, bool ONE_PAGE>
 __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) {
     constexpr int NS = D / 32, NV = D / 16;
     constexpr int KS = D + 8, VS = TILE + 8;                // row strides, elements
@@ -611,7 +658,7 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
     __shared__ __attribute__((aligned(16))) uint16_t sk[2][TILE * KS];
     __shared__ __attribute__((aligned(16))) uint16_t sv[2][D * VS];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), c = lane & 15, g = lane >> 4;
     int id = blockIdx.x;                               // head fastest, then split, row tile, sequence
     const int head = id % a.c.heads;
     id /= a.c.heads;
@@ -623,6 +670,7 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
     const int row0 = (a.tiles - 1 - id % a.tiles) * P_ROWS;     // the last rows see most: they start first
     if (row0 >= rows) return;
     const int shift = 31 - __clz(a.c.page_tokens), in_page = a.c.page_tokens - 1;
+    const bool want_lse = a.lse != nullptr;
     const int32_t* const table = a.c.table + b * a.c.table_stride;
 
     const Span span = span_of(a, s, row0, min(P_ROWS, rows - row0));
@@ -667,23 +715,29 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
     // values, and (for the scales) of this lane's 16 tokens.
     int pk = 0, pv = 0, ps = 0;
     auto pages = [&](int kt) {
-        pk = page_at(a, table, kt + skey, s.len, shift);
-        pv = page_at(a, table, kt + stok, s.len, shift);
-        ps = page_at(a, table, kt + 16 * g, s.len, shift);
+        if constexpr (ONE_PAGE) {
+            pk = pv = ps = uniform(page_at(a, table, kt, s.len, shift));
+        } else {
+            pk = page_at(a, table, kt + skey, s.len, shift);
+            pv = page_at(a, table, kt + stok, s.len, shift);
+            ps = page_at(a, table, kt + 16 * g, s.len, shift);
+        }
     };
-    TileInfo next{};
+    float ks = 0.0f, vs = 0.0f;        // of the tile that is loaded
+    bool present = false;
     auto load = [&](int kt) {
-        if (does_k)
-            kw = *reinterpret_cast<const uint4*>(
-                a.c.k + ((((int64_t)(pk < 0 ? 0 : pk) * a.c.heads + head) << shift) + ((kt + skey) & in_page)) * D + sdim);
-        if (does_v)
-            vw = *reinterpret_cast<const uint4*>(
-                a.c.v + ((((int64_t)(pv < 0 ? 0 : pv) * a.c.heads + head) * D + sd) << shift) + ((kt + stok) & in_page));
+        if (does_k) {
+            const int8_t* page = a.c.k + ((((int64_t)(pk < 0 ? 0 : pk) * a.c.heads + head) << shift)) * D;
+            kw = *reinterpret_cast<const uint4*>(page + ((kt + skey) & in_page) * D + sdim);
+        }
+        if (does_v) {
+            const int8_t* page = a.c.v + (((int64_t)(pv < 0 ? 0 : pv) * a.c.heads + head) << shift) * D;
+            vw = *reinterpret_cast<const uint4*>(page + (sd << shift) + ((kt + stok) & in_page));
+        }
         const int64_t page = (int64_t)(ps < 0 ? 0 : ps) * a.c.heads + head;
-        next.fk = a.c.k_scale[page];
-        next.fv = a.c.v_scale[page];
-        next.key = kt + 16 * g;
-        next.present = ps >= 0;
+        ks = a.c.k_scale[page];
+        vs = a.c.v_scale[page];
+        present = ps >= 0;
     };
     auto store = [&](int buf) {
         if (does_k) {
@@ -708,8 +762,7 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
     for (int kt = k0; kt < k1; kt += TILE, buf ^= 1) {
         __syncthreads();
         const bool more = kt + TILE < k1;
-        TileInfo info = next;
-        info.fk *= a.scale_log2;
+        const TileInfo info = tile_info<ONE_PAGE>(ks, vs, a.scale_log2, kt + 16 * g, present);
         if (more) {
             load(kt + TILE);
             pages(kt + 2 * TILE);
@@ -728,21 +781,23 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
                     for (int t = 0; t < P_QT; ++t) acc[t][j] = mfma(k, qf[t][i], acc[t][j]);
                 }
             }
-            const bool odd =
-                !whole || kt + TILE > wspan.common || kt < wspan.high || __any(!info.present || !(info.fv > 0.0f));
-            info.vmax = group_max(info.fv);
-            f16x8 pf[P_QT][2];
+            const bool plain = whole && kt + TILE <= wspan.common && kt >= wspan.high && plain_tile(info);
+            Weights w[P_QT];
+            float alpha[P_QT];
+            if (plain) {
 #pragma unroll
-            for (int t = 0; t < P_QT; ++t) {
-                uint32_t pw[8];
-                const float alpha = softmax_tile(acc[t], info, !odd, row[t].begin, row[t].end, st[t], pw);
-                if (__any(alpha != 1.0f)) {
+                for (int t = 0; t < P_QT; ++t) alpha[t] = softmax_plain<ONE_PAGE>(acc[t], info, want_lse, st[t], w[t]);
+            } else {
 #pragma unroll
-                    for (int i = 0; i < NV; ++i) o[t][i] *= alpha;
-                }
-                pf[t][0] = __builtin_bit_cast(f16x8, make_uint4(pw[0], pw[1], pw[2], pw[3]));
-                pf[t][1] = __builtin_bit_cast(f16x8, make_uint4(pw[4], pw[5], pw[6], pw[7]));
+                for (int t = 0; t < P_QT; ++t)
+                    alpha[t] = softmax_any(acc[t], info, row[t].begin, row[t].end, st[t], w[t]);
             }
+#pragma unroll
+            for (int t = 0; t < P_QT; ++t)
+                if (__any(alpha[t] != 1.0f)) {
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) o[t][i] *= alpha[t];
+                }
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -750,7 +805,7 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
                     const f16x8 v = __builtin_bit_cast(
                         f16x8, *reinterpret_cast<const uint4*>(&sv[buf][(16 * i + c) * VS + 16 * g + 8 * e]));
 #pragma unroll
-                    for (int t = 0; t < P_QT; ++t) o[t][i] = mfma(v, pf[t][e], o[t][i]);
+                    for (int t = 0; t < P_QT; ++t) o[t][i] = mfma(v, e ? w[t].hi : w[t].lo, o[t][i]);
                 }
         }
         if (more) store(buf ^ 1);
@@ -759,11 +814,11 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
     // lane (c, g) holds columns 16 i + 4 g .. + 3 of its rows
 #pragma unroll
     for (int t = 0; t < P_QT; ++t) {
-        const float l = group_sum(st[t].l), lo = group_sum(st[t].lo);
+        const float l = st[t].l, lo = st[t].lo, vtop = __builtin_amdgcn_exp2f(st[t].lv);
         if (wrow0 + 16 * t + c >= rows) continue;
         const int64_t tok = s.q0 + row[t].token, rid = tok * a.q_heads + row[t].head;
         if (a.splits == 1) {
-            const float inv = l == 0.0f ? 0.0f : st[t].vtop / lo;
+            const float inv = l == 0.0f ? 0.0f : vtop / lo;
             uint16_t* dst = a.out + tok * a.out_stride + (int64_t)row[t].head * D + 4 * g;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -775,7 +830,7 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
         } else {
             float* dst = a.part_o + (rid * a.splits + split) * D + 4 * g;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) *reinterpret_cast<f32x4*>(dst + 16 * i) = o[t][i] * st[t].vtop;
+            for (int i = 0; i < NV; ++i) *reinterpret_cast<f32x4*>(dst + 16 * i) = o[t][i] * vtop;
             if (g == 0) {
                 float* ml = a.part_ml + (rid * a.splits + split) * 4;
                 ml[0] = st[t].m;
@@ -832,6 +887,9 @@ __global__ __launch_bounds__(64) void kv8_join_kernel(AttArgs a) {
 
 // Rows of a block: 256 where a sequence has that many, else 16 (the keys are then split over
 // the waves).
+template <int N>
+using Size = std::integral_constant<int, N>;
+
 bool is_prompt(int64_t max_new, int group) { return max_new * group >= PROMPT_ROWS; }
 int64_t row_tiles(int64_t max_new, int group) {
     const int r = is_prompt(max_new, group) ? P_ROWS : ROWS;
@@ -890,17 +948,27 @@ hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const 
     a.tiles = (int)row_tiles(max_new, a.group);
     a.items = (int)(B * a.tiles);
     const dim3 grid((unsigned)p.blocks), join((unsigned)p.join_blocks);
+    // pages of at least a tile: its page number and scales are one for all lanes
+    auto with_sizes = [&](auto&& go) {
+        const bool one = c.page_tokens >= TILE;
+        if (c.head_dim == 64) { if (one) go(Size<64>{}, std::true_type{}); else go(Size<64>{}, std::false_type{}); }
+        else { if (one) go(Size<128>{}, std::true_type{}); else go(Size<128>{}, std::false_type{}); }
+    };
     if (p.prompt) {
-        if (c.head_dim == 64) hipLaunchKernelGGL(kv8_prompt_kernel<64>, grid, dim3(64 * P_WAVES), 0, stream, a);
-        else hipLaunchKernelGGL(kv8_prompt_kernel<128>, grid, dim3(64 * P_WAVES), 0, stream, a);
+        with_sizes([&](auto d, auto one) {
+            hipLaunchKernelGGL((kv8_prompt_kernel<decltype(d)::value, decltype(one)::value>), grid, dim3(64 * P_WAVES), 0,
+                               stream, a);
+        });
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.join_blocks == 0) return e;
         if (c.head_dim == 64) hipLaunchKernelGGL(kv8_join_kernel<64>, join, dim3(64), 0, stream, a);
         else hipLaunchKernelGGL(kv8_join_kernel<128>, join, dim3(64), 0, stream, a);
         return hipGetLastError();
     }
-    if (c.head_dim == 64) hipLaunchKernelGGL(kv8_attention_kernel<64>, grid, dim3(64 * WAVES), 0, stream, a);
-    else hipLaunchKernelGGL(kv8_attention_kernel<128>, grid, dim3(64 * WAVES), 0, stream, a);
+    with_sizes([&](auto d, auto one) {
+        hipLaunchKernelGGL((kv8_attention_kernel<decltype(d)::value, decltype(one)::value>), grid, dim3(64 * WAVES), 0,
+                           stream, a);
+    });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (c.head_dim == 64) hipLaunchKernelGGL(kv8_join_steps_kernel<64>, join, dim3(64 * WAVES), 0, stream, a);
