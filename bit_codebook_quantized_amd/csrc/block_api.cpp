@@ -210,8 +210,8 @@ int64_t kv8_attention_workspace(int64_t B, int64_t T, int64_t max_new, int64_t m
         return 0;
     max_new = bounded_new(T, max_new);
     if (B == 0 || max_new == 0 || !fits(B, max_new, q_heads)) return 0;
-    return w4a8::attention_workspace(w4a8::attention_plan(B, max_new, max_kv, q_heads, kv_heads, head_dim), T, q_heads,
-                                     head_dim) * (int64_t)sizeof(float);
+    return w4a8::attention_workspace(w4a8::attention_plan(B, max_new, max_kv, q_heads, kv_heads, head_dim), head_dim) *
+           (int64_t)sizeof(float);
 }
 
 int kv8_attention(const void* q, int32_t q_heads, int64_t q_stride, const w4a8_kv8* cache, const int32_t* kv_len,

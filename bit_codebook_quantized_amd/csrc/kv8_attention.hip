@@ -40,7 +40,7 @@ constexpr int ROWS = 16;             // query rows of a block
 constexpr int WAVES = 4;             // waves of a block: they share the rows and split the keys
 constexpr int STEP = TILE * WAVES;   // keys of a block's step
 constexpr float W_EXP = 15.0f;       // weights are kept times 2^15
-constexpr int64_t DEAL_BLOCKS = 512;  // few rows: blocks that share the steps
+constexpr int64_t DEAL_BLOCKS = 512;  // blocks that share the steps: two a CU
 
 struct AttArgs {
     w4a8_kv8 c;
@@ -50,20 +50,25 @@ struct AttArgs {
     const int32_t* kv_len;
     const int32_t* q_start;
     int64_t q_stride, out_stride, T, max_new, window;
-    float* part_o;        // parts: [part row, head_dim], relative to the part's own maximum;
-    float* part_ml;       // [part row, 4]: that maximum (log2 units), the two sums, unused.
-                          // Part rows: many query rows, T * q_heads * splits; few, blocks * 2 * 16
-    int4* part_job;       // few rows, [blocks]: item (-1: nothing to join), head, last block, first slot
+    float* part_o;        // dealt work, parts: [blocks * 2 * rows of a tile, head_dim], relative to
+    float* part_ml;       // the part's own maximum; [.., 4]: that (log2 units), the two sums, unused
+    int4* part_job;       // [blocks]: item (-1: nothing to join), head, last block, first slot
     float scale_log2;     // scale * log2(e)
     int q_heads, group, causal;
     int tiles, items;     // row tiles of a sequence with max_new tokens; of all sequences
-    int splits, chunk;    // keys of a split (a multiple of STEP); the last one takes the rest
 };
 
 // A value that every lane holds, into scalar registers.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int64_t uniform(int64_t v) {
     return (int64_t)((uint64_t)(uint32_t)uniform((int)v) | (uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32);
+}
+
+// The value itself, which the compiler cannot know to be the same in every turn of a loop: what
+// is computed from it is computed anew in each turn instead of being held in registers.
+__device__ __forceinline__ int anew(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
 }
 
 // The query rows of sequence b: how many new tokens, where they start, how long the cache is.
@@ -312,8 +317,8 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l) - W_EXP) * 0.69314718055994531f;
 }
 
-// Few query rows.  The work is a list of steps of 256 keys: for every sequence, row tile (16
-// rows) and head, the steps that its rows see.  The list is dealt to the blocks in equal
+// How the work is dealt.  It is a list of steps: for every sequence, row tile (R rows) and
+// head, the steps of S keys that its rows see.  The list is dealt to the blocks in equal
 // contiguous shares, whatever the sequences' lengths are, so a block holds pieces of a few
 // (row tile, head) pairs; a piece that is not all of one leaves its part in the workspace
 // (a block has at most two such pieces: one that starts its share, one that ends it), and
@@ -323,17 +328,32 @@ struct Item {            // one sequence's row tile
     Span span;
     int row0, rows, steps;    // steps of one head, 0 if the tile has no rows
 };
+template <int R, int S>
 __device__ __forceinline__ Item item_of(const AttArgs& a, int index) {
     Item x;
     x.s = seq_of(a, index / a.tiles);
     x.rows = x.s.n * a.group;
-    x.row0 = (index % a.tiles) * ROWS;
+    x.row0 = (index % a.tiles) * R;
     x.steps = 0;
+    x.span = Span{0, 0, 0, 0};
     if (x.row0 < x.rows) {
-        x.span = span_of(a, x.s, x.row0, min(ROWS, x.rows - x.row0));
-        const int n = (x.span.top + STEP - 1) / STEP - x.span.low / STEP;
+        x.span = span_of(a, x.s, x.row0, min(R, x.rows - x.row0));
+        const int n = (x.span.top + S - 1) / S - x.span.low / S;
         x.steps = n > 0 ? n : 1;
     }
+    return x;
+}
+
+// The item at the same index in every lane, in scalar registers.
+template <int R, int S>
+__device__ __forceinline__ Item one_item(const AttArgs& a, int index) {
+    const Item v = item_of<R, S>(a, index);
+    Item x;
+    x.s = Seq{uniform(v.s.q0), uniform(v.s.n), uniform(v.s.len), uniform(v.s.pos0)};
+    x.span = Span{uniform(v.span.low), uniform(v.span.top), uniform(v.span.high), uniform(v.span.common)};
+    x.row0 = uniform(v.row0);
+    x.rows = uniform(v.rows);
+    x.steps = uniform(v.steps);
     return x;
 }
 
@@ -347,10 +367,11 @@ __device__ __forceinline__ int64_t wave_prefix(int64_t v, int lane) {      // in
 }
 
 // Steps of all items (whole wave).
+template <int R, int S>
 __device__ __forceinline__ int64_t total_steps(const AttArgs& a, int lane) {
     int64_t sum = 0;
     for (int i = 0; i < a.items; i += 64) {
-        int64_t v = i + lane < a.items ? (int64_t)item_of(a, i + lane).steps * a.c.heads : 0;
+        int64_t v = i + lane < a.items ? (int64_t)item_of<R, S>(a, i + lane).steps * a.c.heads : 0;
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
         sum += v;
@@ -383,10 +404,11 @@ __device__ __forceinline__ Shares shares_of(int64_t total, int64_t blocks) {
 }
 
 // The item that holds position `at` of the list (at < total), and where it starts.
+template <int R, int S>
 __device__ __forceinline__ int item_at(const AttArgs& a, int64_t at, int lane, int64_t& before) {
     int64_t sum = 0;
     for (int i = 0; i < a.items; i += 64) {
-        const int64_t v = i + lane < a.items ? (int64_t)item_of(a, i + lane).steps * a.c.heads : 0;
+        const int64_t v = i + lane < a.items ? (int64_t)item_of<R, S>(a, i + lane).steps * a.c.heads : 0;
         const int64_t p = sum + wave_prefix(v, lane);
         const uint64_t past = __ballot(p > at);
         if (past != 0) {
@@ -400,10 +422,93 @@ __device__ __forceinline__ int item_at(const AttArgs& a, int64_t at, int lane, i
     return a.items;
 }
 
+// One block's share, piece by piece.
+struct Piece {
+    int index, head, step, steps;      // item, head, first step and how many
+    int64_t slot;                      // part row of its first row, if it is not all of the item's steps
+    bool whole;
+};
+template <int R, int S>
+struct Walk {
+    Shares deal;
+    int64_t from, to, at, before;
+    int index;
+
+    // Whether this block has a share.
+    __device__ __forceinline__ bool begin(const AttArgs& a, int lane) {
+        deal = shares_of(total_steps<R, S>(a, lane), gridDim.x);
+        if (blockIdx.x >= deal.blocks) return false;
+        from = at = deal.from(blockIdx.x);
+        to = deal.from(blockIdx.x + 1);
+        index = item_at<R, S>(a, from, lane, before);
+        return true;
+    }
+    // The next piece and its item.
+    __device__ __forceinline__ bool next(const AttArgs& a, Piece& p, Item& x) {
+        while (at < to && index < a.items) {
+            x = one_item<R, S>(a, index);
+            const int64_t size = (int64_t)x.steps * a.c.heads;
+            if (at >= before + size) {         // this item is done (or has no rows)
+                before += size;
+                ++index;
+                continue;
+            }
+            p.index = index;
+            p.head = (int)quotient(at - before, x.steps);
+            p.step = (int)((at - before) - (int64_t)p.head * x.steps);
+            p.steps = (int)(to - at < x.steps - p.step ? to - at : x.steps - p.step);
+            p.whole = p.steps == x.steps;
+            p.slot = (2 * (int64_t)blockIdx.x + (at == from ? 0 : 1)) * R;
+            // The piece that begins a row tile and head, and does not end it, names who joins the
+            // parts: this block, up to the last block that has one.
+            if (threadIdx.x == 0 && p.step == 0 && !p.whole)
+                a.part_job[blockIdx.x] =
+                    make_int4(index, p.head, (int)deal.block_of(at + x.steps - 1), at == from ? 0 : 1);
+            at += p.steps;
+            return true;
+        }
+        return false;
+    }
+    // Between pieces the state lies in LDS, a copy a wave, and not in registers.
+    __device__ __forceinline__ void keep(Walk& lds) const {
+        lds = *this;
+        wave_lds_sync();
+    }
+};
+
+template <int R, int S>
+__device__ __forceinline__ bool next_piece(const AttArgs& a, Walk<R, S>& lds, Piece& p, Item& x) {
+    Walk<R, S> w;
+    w.deal = Shares{uniform(lds.deal.blocks), uniform(lds.deal.each), uniform(lds.deal.rest)};
+    w.from = uniform(lds.from);
+    w.to = uniform(lds.to);
+    w.at = uniform(lds.at);
+    w.before = uniform(lds.before);
+    w.index = uniform(lds.index);
+    const bool more = w.next(a, p, x);
+    w.keep(lds);
+    return more;
+}
+
+// Without dealing: block i takes all of one (row tile, head) pair, heads fastest, and the last
+// row tiles of a sequence first (causal rows see more the later they are).
+template <int R, int S>
+__device__ __forceinline__ bool own_item(const AttArgs& a, Piece& p, Item& x) {
+    const int i = blockIdx.x / a.c.heads;
+    p.head = blockIdx.x % a.c.heads;
+    p.index = i / a.tiles * a.tiles + a.tiles - 1 - i % a.tiles;
+    x = one_item<R, S>(a, p.index);
+    p.step = 0;
+    p.steps = x.steps;
+    p.slot = 0;
+    p.whole = true;
+    return x.steps > 0;
+}
+
 // A wave loads its tile straight into registers in the order of the matrix operands: the
 // values of a tile while its scores are made, the keys of the next one while its weights are
 // used.  The four waves take the step's four tiles and are joined through LDS.
-template <int D, bool ONE_PAGE>
+template <int D, bool ONE_PAGE, bool DEAL>
 __global__ __launch_bounds__(64 * WAVES, 2) void kv8_attention_kernel(AttArgs a) {
     constexpr int NK = D / 64;       // 16-byte key loads a lane and sub-tile
     constexpr int NV = D / 16;       // value column tiles
@@ -411,34 +516,32 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv8_attention_kernel(AttArgs a)
     __shared__ float so[WAVES][D][ROWS + 1];
     __shared__ float sm[WAVES][ROWS], sl[WAVES][ROWS], slo[WAVES][ROWS];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), c = lane & 15, g = lane >> 4;
-    const Shares deal = shares_of(total_steps(a, lane), gridDim.x);
-    if (tid == 0) a.part_job[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    if (blockIdx.x >= deal.blocks) return;
-    const int64_t from = deal.from(blockIdx.x), to = deal.from(blockIdx.x + 1);
-    int64_t before;
-    int index = item_at(a, from, lane, before);
+    __shared__ Walk<ROWS, STEP> walks[WAVES];
+    const int wave = uniform((int)threadIdx.x >> 6);
+    Piece piece;
+    Item x;
+    if constexpr (DEAL) {
+        if (threadIdx.x == 0) a.part_job[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        Walk<ROWS, STEP> walk;
+        if (!walk.begin(a, threadIdx.x & 63) || !walk.next(a, piece, x)) return;
+        walk.keep(walks[wave]);
+    } else if (!own_item<ROWS, STEP>(a, piece, x)) {
+        return;
+    }
     const int shift = 31 - __clz(a.c.page_tokens), in_page = a.c.page_tokens - 1;
     const bool want_lse = a.lse != nullptr;
 
-    for (int64_t at = from; at < to && index < a.items;) {
-        const Item x = item_of(a, index);
-        const int64_t size = (int64_t)x.steps * a.c.heads;
-        if (at >= before + size) {         // this item is done (or has no rows)
-            before += size;
-            ++index;
-            continue;
-        }
-        const int head = (int)quotient(at - before, x.steps), step = (int)((at - before) - (int64_t)head * x.steps);
-        const int steps = (int)(to - at < x.steps - step ? to - at : x.steps - step);
+    do {
+        const int tid = DEAL ? anew(threadIdx.x) : threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+        const int head = piece.head;
         const Seq& s = x.s;
         const Span& span = x.span;
         const int rows = x.rows, row0 = x.row0;
-        const int32_t* const table = a.c.table + (int64_t)(index / a.tiles) * a.c.table_stride;
+        const int32_t* const table = a.c.table + (int64_t)(piece.index / a.tiles) * a.c.table_stride;
         const Row row = row_of(a, s, head, row0 + c, rows);
         const bool whole = row0 + ROWS <= rows;
-        const int first = (span.low / STEP + step) * STEP;
-        const int k0 = first + wave * TILE, k1 = min(span.top, first + steps * STEP);
+        const int first = (span.low / STEP + piece.step) * STEP;
+        const int k0 = first + wave * TILE, k1 = min(span.top, first + piece.steps * STEP);
 
         bf16x8 qf[2 * NK];
         {
@@ -538,10 +641,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv8_attention_kernel(AttArgs a)
                 lt += sl[w][r] * f[w];
                 lot += slo[w][r] * f[w];
             }
-            const bool final = steps == x.steps;
             const int out_token = (row0 + r) / a.group, out_head = head * a.group + (row0 + r) % a.group;
             const int64_t t = s.q0 + out_token, rid = t * a.q_heads + out_head;
-            const int64_t slot = (2 * (int64_t)blockIdx.x + (at == from ? 0 : 1)) * ROWS + r;
+            const int64_t slot = piece.slot + r;
             const float inv = lt == 0.0f ? 0.0f : 1.0f / lot;      // a row that sees no key: 0
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -549,38 +651,34 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv8_attention_kernel(AttArgs a)
                 float v = 0.0f;
 #pragma unroll
                 for (int w = 0; w < WAVES; ++w) v = __builtin_fmaf(so[w][d][r], f[w], v);
-                if (final) a.out[t * a.out_stride + (int64_t)out_head * D + d] = f32_to_bf16(lt == 0.0f ? 0.0f : v * inv);
+                if (!DEAL || piece.whole) a.out[t * a.out_stride + (int64_t)out_head * D + d] = f32_to_bf16(lt == 0.0f ? 0.0f : v * inv);
                 else a.part_o[slot * D + d] = v;
             }
             if (d0 == 0) {
-                if (!final) *reinterpret_cast<float4*>(a.part_ml + slot * 4) = make_float4(mt, lt, lot, 0.0f);
+                if (DEAL && !piece.whole) *reinterpret_cast<float4*>(a.part_ml + slot * 4) = make_float4(mt, lt, lot, 0.0f);
                 else if (a.lse) a.lse[rid] = lse_of(mt, lt);
             }
         }
-        // The piece that begins a row tile and head, and does not end it, names who joins the
-        // parts: this block's number and the last block that has one.
-        if (tid == 0 && step == 0 && steps < x.steps)
-            a.part_job[blockIdx.x] = make_int4(index, head, (int)deal.block_of(at + x.steps - 1), at == from ? 0 : 1);
         __syncthreads();       // before the next piece's results
-        at += steps;
-    }
+    } while (DEAL && next_piece(a, walks[wave], piece, x));
 }
 
-// Joins the parts of the row tile and head that block blockIdx.x of the main launch began: the
-// waves take parts in turn with a running maximum, then join through LDS.  A lane has 4 columns
-// of every 64 / (D / 4)-th row.
-template <int D>
-__global__ __launch_bounds__(64 * WAVES) void kv8_join_steps_kernel(AttArgs a) {
+// Joins the parts of the row tile and head that one block of the main launch began, 16 rows a
+// block: the waves take parts in turn with a running maximum, then join through LDS.  A lane has
+// 4 columns of every 64 / (D / 4)-th row.
+template <int D, int R, int S>
+__global__ __launch_bounds__(64 * WAVES) void kv8_join_kernel(AttArgs a) {
     constexpr int LANES = D / 4, AT_ONCE = 64 / LANES, NR = ROWS / AT_ONCE;
     __shared__ __attribute__((aligned(16))) float so[WAVES][ROWS][D];
     __shared__ float sm[WAVES][ROWS], sl[WAVES][ROWS], slo[WAVES][ROWS];
-    const int4 job = a.part_job[blockIdx.x];
+    const int first = blockIdx.x / (R / ROWS), sub0 = blockIdx.x % (R / ROWS) * ROWS;
+    const int4 job = a.part_job[first];
     if (job.x < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int sub = lane / LANES, col = 4 * (lane % LANES);
-    const Item x = item_of(a, job.x);
-    const int count = min(ROWS, x.rows - x.row0);
-    const int first = blockIdx.x, last = job.z;
+    const Item x = one_item<R, S>(a, uniform(job.x));
+    const int count = min(ROWS, x.rows - x.row0 - sub0), last = job.z;
+    if (count <= 0) return;
 
     f32x4 v[NR];
     float m[NR], l[NR], lo[NR];
@@ -591,7 +689,7 @@ __global__ __launch_bounds__(64 * WAVES) void kv8_join_steps_kernel(AttArgs a) {
         l[j] = lo[j] = 0.0f;
     }
     for (int i = first + wave; i <= last; i += WAVES) {
-        const int64_t slot = (2 * (int64_t)i + (i == first ? job.w : 0)) * ROWS;
+        const int64_t slot = (2 * (int64_t)i + (i == first ? job.w : 0)) * R + sub0;
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
             const int r = AT_ONCE * j + sub;
@@ -632,8 +730,8 @@ __global__ __launch_bounds__(64 * WAVES) void kv8_join_steps_kernel(AttArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(p[e], f, y[e]);
         }
-        const int64_t t = x.s.q0 + (x.row0 + r) / a.group;
-        const int qh = job.y * a.group + (x.row0 + r) % a.group;
+        const int64_t t = x.s.q0 + (x.row0 + sub0 + r) / a.group;
+        const int qh = job.y * a.group + (x.row0 + sub0 + r) % a.group;
         const float inv = 1.0f / lot;
         *reinterpret_cast<uint2*>(a.out + t * a.out_stride + (int64_t)qh * D + d) =
             lt == 0.0f ? make_uint2(0, 0) : make_uint2(f32x2_to_bf16x2(y[0] * inv, y[1] * inv), f32x2_to_bf16x2(y[2] * inv, y[3] * inv));
@@ -641,42 +739,57 @@ __global__ __launch_bounds__(64 * WAVES) void kv8_join_steps_kernel(AttArgs a) {
     }
 }
 
-// Many query rows: a block has 256 of them, 32 a wave, and all its waves walk the same keys.
+// Place of 16-byte piece p of row r of an LDS tile whose rows have W pieces (8 or 16): the
+// pieces are exchanged among the rows that share banks (256 bytes), so that the 16 lanes that
+// read one piece of 16 consecutive rows each meet every bank once.
+template <int W>
+__device__ __forceinline__ int lds_piece(int r, int p) {
+    static_assert(W == 8 || W == 16, "128- or 256-byte rows");
+    return W * r + (p ^ (W == 16 ? r & 15 : (r >> 1) & 7));
+}
+
+// Many query rows: a block has 128 of them, 32 a wave, and all its waves walk the same keys.
 // A tile is widened once a block on its way into LDS (two tiles in turn: the next one is
 // loaded while this one is used, one barrier a tile).  A key lies at row 16 j + 4 a + b of the
-// tile for key 16 a + 4 j + b, so that the 16 rows of a sub-tile follow each other; rows are
-// padded by 16 bytes, and 16 lanes reading 16 bytes each from consecutive rows meet no bank
-// twice.
+// tile for key 16 a + 4 j + b, so that the 16 rows of a sub-tile follow each other; tokens
+// 16 g + 8 e .. + 7 of a value column are its piece 4 e + g.  Two blocks share a CU and are not
+// in step, so one's matrix work meets the other's vector work (one block of 256 rows, whose
+// waves pass the barrier together, was 5 % faster on 4096 of 16384 tokens and 15 to 30 %
+// slower on prompts of 2000).  The loop is near three limits at once, matrix instructions, LDS
+// reads and vector instructions (about 2100, 2300 and 2800 cycles a tile and CU); reads
+// are issued four ahead of the products that use them, which the compiler does not do itself.
 constexpr int PROMPT_ROWS = 128;     // from this many rows of a sequence on
-constexpr int P_WAVES = 8, P_QT = 2, P_ROWS = 16 * P_QT * P_WAVES;
+constexpr int P_WAVES = 4, P_QT = 2, P_ROWS = 16 * P_QT * P_WAVES;
 
-template <int D, bool ONE_PAGE>
+template <int D, bool ONE_PAGE, bool DEAL>
 __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) {
     constexpr int NS = D / 32, NV = D / 16;
-    constexpr int KS = D + 8, VS = TILE + 8;                // row strides, elements
     constexpr int CHUNKS = TILE * D / 16;                   // 16-code pieces of a tile's keys, or values
-    __shared__ __attribute__((aligned(16))) uint16_t sk[2][TILE * KS];
-    __shared__ __attribute__((aligned(16))) uint16_t sv[2][D * VS];
+    __shared__ __attribute__((aligned(16))) uint16_t sk[2][TILE * D];
+    __shared__ __attribute__((aligned(16))) uint16_t sv[2][D * TILE];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), c = lane & 15, g = lane >> 4;
-    int id = blockIdx.x;                               // head fastest, then split, row tile, sequence
-    const int head = id % a.c.heads;
-    id /= a.c.heads;
-    const int split = id % a.splits;
-    id /= a.splits;
-    const int64_t b = id / a.tiles;
-    const Seq s = seq_of(a, b);
-    const int rows = s.n * a.group;
-    const int row0 = (a.tiles - 1 - id % a.tiles) * P_ROWS;     // the last rows see most: they start first
-    if (row0 >= rows) return;
+    const int wave = uniform((int)threadIdx.x >> 6);
     const int shift = 31 - __clz(a.c.page_tokens), in_page = a.c.page_tokens - 1;
     const bool want_lse = a.lse != nullptr;
-    const int32_t* const table = a.c.table + b * a.c.table_stride;
-
-    const Span span = span_of(a, s, row0, min(P_ROWS, rows - row0));
-    const int k_first = split * a.chunk;
-    const int k0 = max(k_first, span.low / TILE * TILE);
-    const int k1 = split == a.splits - 1 ? span.top : min(span.top, k_first + a.chunk);
+    __shared__ Walk<P_ROWS, TILE> walks[P_WAVES];
+    Piece job;
+    Item x;
+    if constexpr (DEAL) {
+        if (threadIdx.x == 0) a.part_job[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        Walk<P_ROWS, TILE> walk;
+        if (!walk.begin(a, threadIdx.x & 63) || !walk.next(a, job, x)) return;
+        walk.keep(walks[wave]);
+    } else if (!own_item<P_ROWS, TILE>(a, job, x)) {
+        return;
+    }
+    do {
+    const int tid = DEAL ? anew(threadIdx.x) : threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const int head = job.head;
+    const Seq& s = x.s;
+    const Span& span = x.span;
+    const int rows = x.rows, row0 = x.row0;
+    const int32_t* const table = a.c.table + (int64_t)(job.index / a.tiles) * a.c.table_stride;
+    const int k0 = (span.low / TILE + job.step) * TILE, k1 = min(span.top, k0 + job.steps * TILE);
 
     // this wave's rows
     const int wrow0 = row0 + 16 * P_QT * wave;
@@ -701,24 +814,25 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
         for (int i = 0; i < NV; ++i) o[t][i] = f32x4{0, 0, 0, 0};
     }
 
-    // This thread's piece of the staged tile.  D = 128: 16 codes of a key and 16 of a value column;
-    // D = 64: one of the two.
-    constexpr bool BOTH = CHUNKS == 64 * P_WAVES;
-    static_assert(BOTH || 2 * CHUNKS == 64 * P_WAVES, "a tile is one or two pieces a thread");
-    const bool does_k = BOTH || tid < CHUNKS, does_v = BOTH || tid >= CHUNKS;
-    const int piece = tid & (CHUNKS - 1);
-    const int skey = piece / (D / 16), sdim = 16 * (piece % (D / 16));          // key of the tile, first dim
-    const int sd = piece >> 2, stok = 16 * (piece & 3);                         // value column, first token
-    const int krow = 16 * ((skey >> 2) & 3) + 4 * (skey >> 4) + (skey & 3);
-    uint4 kw = make_uint4(0, 0, 0, 0), vw = make_uint4(0, 0, 0, 0);
+    // This thread's pieces of the staged tile: 16 codes of a key, and 16 of a value column.
+    constexpr int NP = CHUNKS / (64 * P_WAVES);
+    static_assert(NP * 64 * P_WAVES == CHUNKS, "whole pieces a thread");
+    auto piece_key = [&](int p) { return (tid + 64 * P_WAVES * p) / (D / 16); };
+    auto piece_dim = [&](int p) { return 16 * ((tid + 64 * P_WAVES * p) % (D / 16)); };
+    auto piece_col = [&](int p) { return (tid + 64 * P_WAVES * p) >> 2; };
+    const int stok = 16 * (tid & 3);
+    uint4 kw[NP], vw[NP];
     // Page numbers are fetched a tile before what they point at: of the staged piece's keys and
     // values, and (for the scales) of this lane's 16 tokens.
-    int pk = 0, pv = 0, ps = 0;
+    int pk[NP] = {}, pv = 0, ps = 0;
     auto pages = [&](int kt) {
         if constexpr (ONE_PAGE) {
-            pk = pv = ps = uniform(page_at(a, table, kt, s.len, shift));
+            pv = ps = uniform(page_at(a, table, kt, s.len, shift));
+#pragma unroll
+            for (int p = 0; p < NP; ++p) pk[p] = pv;
         } else {
-            pk = page_at(a, table, kt + skey, s.len, shift);
+#pragma unroll
+            for (int p = 0; p < NP; ++p) pk[p] = page_at(a, table, kt + piece_key(p), s.len, shift);
             pv = page_at(a, table, kt + stok, s.len, shift);
             ps = page_at(a, table, kt + 16 * g, s.len, shift);
         }
@@ -726,40 +840,73 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
     float ks = 0.0f, vs = 0.0f;        // of the tile that is loaded
     bool present = false;
     auto load = [&](int kt) {
-        if (does_k) {
-            const int8_t* page = a.c.k + ((((int64_t)(pk < 0 ? 0 : pk) * a.c.heads + head) << shift)) * D;
-            kw = *reinterpret_cast<const uint4*>(page + ((kt + skey) & in_page) * D + sdim);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int8_t* page = a.c.k + ((((int64_t)(pk[p] < 0 ? 0 : pk[p]) * a.c.heads + head) << shift)) * D;
+            kw[p] = *reinterpret_cast<const uint4*>(page + ((kt + piece_key(p)) & in_page) * D + piece_dim(p));
         }
-        if (does_v) {
-            const int8_t* page = a.c.v + (((int64_t)(pv < 0 ? 0 : pv) * a.c.heads + head) << shift) * D;
-            vw = *reinterpret_cast<const uint4*>(page + (sd << shift) + ((kt + stok) & in_page));
-        }
+        const int8_t* values = a.c.v + (((int64_t)(pv < 0 ? 0 : pv) * a.c.heads + head) << shift) * D;
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+            vw[p] = *reinterpret_cast<const uint4*>(values + (piece_col(p) << shift) + ((kt + stok) & in_page));
         const int64_t page = (int64_t)(ps < 0 ? 0 : ps) * a.c.heads + head;
         ks = a.c.k_scale[page];
         vs = a.c.v_scale[page];
         present = ps >= 0;
     };
-    auto store = [&](int buf) {
-        if (does_k) {
-            uint4* dst = reinterpret_cast<uint4*>(&sk[buf][krow * KS + sdim]);
-            dst[0] = __builtin_bit_cast(uint4, widen(kw.x, kw.y));
-            dst[1] = __builtin_bit_cast(uint4, widen(kw.z, kw.w));
+    auto store = [&](int kbuf, int vbuf) {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int key = piece_key(p), row = 16 * ((key >> 2) & 3) + 4 * (key >> 4) + (key & 3), at = piece_dim(p) / 8;
+            uint4* k = reinterpret_cast<uint4*>(sk[kbuf]);
+            k[lds_piece<D / 8>(row, at)] = __builtin_bit_cast(uint4, widen(kw[p].x, kw[p].y));
+            k[lds_piece<D / 8>(row, at + 1)] = __builtin_bit_cast(uint4, widen(kw[p].z, kw[p].w));
+            uint4* v = reinterpret_cast<uint4*>(sv[vbuf]);
+            v[lds_piece<8>(piece_col(p), stok / 16)] = __builtin_bit_cast(uint4, widen_f16(vw[p].x, vw[p].y));
+            v[lds_piece<8>(piece_col(p), stok / 16 + 4)] = __builtin_bit_cast(uint4, widen_f16(vw[p].z, vw[p].w));
         }
-        if (does_v) {
-            uint4* dst = reinterpret_cast<uint4*>(&sv[buf][sd * VS + stok]);
-            dst[0] = __builtin_bit_cast(uint4, widen_f16(vw.x, vw.y));
-            dst[1] = __builtin_bit_cast(uint4, widen_f16(vw.z, vw.w));
+    };
+
+    // The weights of a tile that this wave has not yet used.
+    Weights w[P_QT];
+    float alpha[P_QT];
+    auto use_weights = [&](int vbuf) {
+#pragma unroll
+        for (int t = 0; t < P_QT; ++t)
+            if (__any(alpha[t] != 1.0f)) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) o[t][i] *= alpha[t];
+            }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const f16x8 v = __builtin_bit_cast(
+                    f16x8, reinterpret_cast<const uint4*>(sv[vbuf])[lds_piece<8>(c, 4 * e + g) + 16 * 8 * i]);
+#pragma unroll
+                for (int t = 0; t < P_QT; ++t) o[t][i] = mfma(v, e ? w[t].hi : w[t].lo, o[t][i]);
+            }
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * NV - 4; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, P_QT, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
+        __builtin_amdgcn_sched_group_barrier(0x008, 4 * P_QT, 0);
     };
 
     if (k0 < k1) {
         pages(k0);
         load(k0);
         pages(k0 + TILE);
-        store(0);
+        store(0, 0);
     }
-    int buf = 0;
-    for (int kt = k0; kt < k1; kt += TILE, buf ^= 1) {
+    // The queries have arrived: a wait for them inside the loop would wait for the tile that is
+    // being fetched as well.
+    __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0)
+    int kbuf = 0, vbuf = 0;             // of this tile
+    for (int kt = k0; kt < k1; kt += TILE) {
+        const int vnext = vbuf ^ 1;
         __syncthreads();
         const bool more = kt + TILE < k1;
         const TileInfo info = tile_info<ONE_PAGE>(ks, vs, a.scale_log2, kt + 16 * g, present);
@@ -776,14 +923,19 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
                     const bf16x8 k = __builtin_bit_cast(
-                        bf16x8, *reinterpret_cast<const uint4*>(&sk[buf][(16 * j + c) * KS + 32 * i + 8 * g]));
+                        bf16x8, reinterpret_cast<const uint4*>(sk[kbuf])[lds_piece<D / 8>(c, 4 * i + g) + 16 * (D / 8) * j]);
 #pragma unroll
                     for (int t = 0; t < P_QT; ++t) acc[t][j] = mfma(k, qf[t][i], acc[t][j]);
                 }
             }
+            __builtin_amdgcn_sched_group_barrier(0x100, 4, 1);
+#pragma unroll
+            for (int i = 0; i < 4 * NS - 4; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, P_QT, 1);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, 4 * P_QT, 1);
             const bool plain = whole && kt + TILE <= wspan.common && kt >= wspan.high && plain_tile(info);
-            Weights w[P_QT];
-            float alpha[P_QT];
             if (plain) {
 #pragma unroll
                 for (int t = 0; t < P_QT; ++t) alpha[t] = softmax_plain<ONE_PAGE>(acc[t], info, want_lse, st[t], w[t]);
@@ -792,23 +944,11 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
                 for (int t = 0; t < P_QT; ++t)
                     alpha[t] = softmax_any(acc[t], info, row[t].begin, row[t].end, st[t], w[t]);
             }
-#pragma unroll
-            for (int t = 0; t < P_QT; ++t)
-                if (__any(alpha[t] != 1.0f)) {
-#pragma unroll
-                    for (int i = 0; i < NV; ++i) o[t][i] *= alpha[t];
-                }
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const f16x8 v = __builtin_bit_cast(
-                        f16x8, *reinterpret_cast<const uint4*>(&sv[buf][(16 * i + c) * VS + 16 * g + 8 * e]));
-#pragma unroll
-                    for (int t = 0; t < P_QT; ++t) o[t][i] = mfma(v, e ? w[t].hi : w[t].lo, o[t][i]);
-                }
+            use_weights(vbuf);
         }
-        if (more) store(buf ^ 1);
+        if (more) store(kbuf ^ 1, vnext);
+        kbuf ^= 1;
+        vbuf = vnext;
     }
 
     // lane (c, g) holds columns 16 i + 4 g .. + 3 of its rows
@@ -816,76 +956,31 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
     for (int t = 0; t < P_QT; ++t) {
         const float l = st[t].l, lo = st[t].lo, vtop = __builtin_amdgcn_exp2f(st[t].lv);
         if (wrow0 + 16 * t + c >= rows) continue;
-        const int64_t tok = s.q0 + row[t].token, rid = tok * a.q_heads + row[t].head;
-        if (a.splits == 1) {
+        const Row mine = row_of(a, s, head, wrow0 + 16 * t + c, rows);
+        const int64_t tok = s.q0 + mine.token;
+        if (!DEAL || job.whole) {
             const float inv = l == 0.0f ? 0.0f : vtop / lo;
-            uint16_t* dst = a.out + tok * a.out_stride + (int64_t)row[t].head * D + 4 * g;
+            uint16_t* dst = a.out + tok * a.out_stride + (int64_t)mine.head * D + 4 * g;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const f32x4 v = o[t][i] * inv;
                 *reinterpret_cast<uint2*>(dst + 16 * i) =
                     l == 0.0f ? make_uint2(0, 0) : make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
             }
-            if (a.lse && g == 0) a.lse[rid] = lse_of(st[t].m, l);
+            if (want_lse && g == 0) a.lse[tok * a.q_heads + mine.head] = lse_of(st[t].m, l);
         } else {
-            float* dst = a.part_o + (rid * a.splits + split) * D + 4 * g;
+            const int64_t slot = job.slot + 16 * (P_QT * wave + t) + c;
+            float* dst = a.part_o + slot * D + 4 * g;
 #pragma unroll
             for (int i = 0; i < NV; ++i) *reinterpret_cast<f32x4*>(dst + 16 * i) = o[t][i] * vtop;
-            if (g == 0) {
-                float* ml = a.part_ml + (rid * a.splits + split) * 4;
-                ml[0] = st[t].m;
-                ml[1] = l;
-                ml[2] = lo;
-            }
+            if (g == 0) *reinterpret_cast<float4*>(a.part_ml + slot * 4) = make_float4(st[t].m, l, lo, 0.0f);
         }
     }
+    __syncthreads();       // the tiles in LDS are free again
+    } while (DEAL && next_piece(a, walks[wave], job, x));
 }
 
-// Joins the splits of one query row: a wave a row, lane i holds split i's maximum and sums
-// (at most 64 splits).
-template <int D>
-__global__ __launch_bounds__(64) void kv8_join_kernel(AttArgs a) {
-    int bid = blockIdx.x;
-    const int lane = threadIdx.x, head = bid % a.c.heads;
-    bid /= a.c.heads;
-    const int most = (int)a.max_new * a.group, row = bid % most;
-    const int64_t b = bid / most;
-    const Seq s = seq_of(a, b);
-    if (row >= s.n * a.group) return;
-    const int64_t t = s.q0 + row / a.group;
-    const int qh = head * a.group + row % a.group;
-    const int64_t id = t * a.q_heads + qh;
-    const float* po = a.part_o + id * a.splits * D;
-    float4 ml = make_float4(-__builtin_inff(), 0.0f, 0.0f, 0.0f);
-    if (lane < a.splits) ml = *reinterpret_cast<const float4*>(a.part_ml + (id * a.splits + lane) * 4);
-    float mt = ml.x;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) mt = __builtin_fmaxf(mt, __shfl_xor(mt, o));
-    const float ref = mt > -__builtin_inff() ? mt : 0.0f;
-    const float f = __builtin_amdgcn_exp2f(ml.x - ref);
-    float lt = ml.y * f, lot = ml.z * f;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        lt += __shfl_xor(lt, o);
-        lot += __shfl_xor(lot, o);
-    }
-    float v[D / 64];
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j) v[j] = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < a.splits; ++i) {
-        const float w = __shfl(f, i);
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) v[j] = __builtin_fmaf(po[(int64_t)i * D + lane + 64 * j], w, v[j]);
-    }
-    const float inv = 1.0f / lot;
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j)
-        a.out[t * a.out_stride + (int64_t)qh * D + lane + 64 * j] = f32_to_bf16(lt == 0.0f ? 0.0f : v[j] * inv);
-    if (a.lse && lane == 0) a.lse[id] = lse_of(mt, lt);
-}
-
-// Rows of a block: 256 where a sequence has that many, else 16 (the keys are then split over
+// Rows of a block: 128 where a sequence has that many, else 16 (the keys are then split over
 // the waves).
 template <int N>
 using Size = std::integral_constant<int, N>;
@@ -898,31 +993,32 @@ int64_t row_tiles(int64_t max_new, int group) {
 
 }  // namespace
 
-// Blocks of a launch, and for many rows the splits of the context.  Few rows: two blocks a CU,
-// as many as fit at once, or one for each step if there are fewer.  Many: enough splits for a
-// block a CU, none below eight tiles.
+// Blocks of a launch: one for each (row tile, head), or 512 (two a CU, as many as fit at once)
+// that share all steps equally and whose parts are then joined.  Dealing costs the parts'
+// traffic and a second launch, and pays where the pairs leave blocks idle for long: measured
+// with 128 rows, by about ten steps of 64 keys (1 x 500 of 500 tokens, 32 heads: 29 us a
+// block each, 46 us dealt; 4 x 300 of 2048: 98 and 72 us; 4 x 128 of 8192: 153 and 87 us).
+// With few rows a step is 256 keys, and lengths are uneven as a rule, so long contexts are
+// dealt however many pairs there are (16 x up to 32 k tokens: 181 us in fixed splits, 115
+// dealt; 256 x up to 400: 57 us dealt, 34 us a block each).  There are never
+// more blocks than steps (few rows) or a quarter of that (128 rows).
 AttentionPlan attention_plan(int64_t B, int64_t max_new, int64_t max_kv, int q_heads, int kv_heads, int head_dim) {
     const int group = q_heads / kv_heads;
     AttentionPlan p{};
     p.prompt = is_prompt(max_new, group);
-    const int64_t base = B * kv_heads * row_tiles(max_new, group);
-    if (p.prompt) {
-        p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(64, std::min(256 / std::max<int64_t>(1, base), max_kv / (8 * TILE))));
-        p.blocks = base * p.splits;
-        p.join_blocks = p.splits > 1 ? B * max_new * q_heads : 0;
-        p.part_rows = p.splits > 1 ? p.splits : 0;          // times the rows of q
-        return p;
-    }
-    p.splits = 1;
-    p.blocks = std::min<int64_t>(DEAL_BLOCKS, base * std::max<int64_t>(1, (max_kv + STEP - 1) / STEP));
-    p.join_blocks = p.blocks;
-    p.part_rows = p.blocks * 2 * ROWS;
+    const int64_t base = B * kv_heads * row_tiles(max_new, group), rows = p.prompt ? P_ROWS : ROWS;
+    const int64_t steps = std::max<int64_t>(1, p.prompt ? max_kv / TILE : (max_kv + STEP - 1) / STEP);
+    const int64_t idle = steps * std::max<int64_t>(0, DEAL_BLOCKS - base);      // in steps of all blocks
+    p.deal = p.prompt ? idle >= 10 * DEAL_BLOCKS : steps >= 8 || idle >= 3 * DEAL_BLOCKS;
+    p.blocks = p.deal ? std::min<int64_t>(DEAL_BLOCKS, base * (p.prompt ? (steps + 3) / 4 : steps)) : base;
+    p.join_blocks = p.deal ? p.blocks * (rows / ROWS) : 0;
+    p.part_rows = p.deal ? p.blocks * 2 * rows : 0;
     return p;
 }
 
 // Floats of workspace.
-int64_t attention_workspace(const AttentionPlan& p, int64_t T, int q_heads, int head_dim) {
-    return (p.prompt ? T * q_heads * p.part_rows : p.part_rows) * (head_dim + 4) + (p.prompt ? 0 : 4 * p.blocks);
+int64_t attention_workspace(const AttentionPlan& p, int head_dim) {
+    return p.deal ? p.part_rows * (head_dim + 4) + 4 * p.blocks : 0;
 }
 
 hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const w4a8_kv8& c, const int32_t* kv_len,
@@ -940,11 +1036,9 @@ hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const 
     a.scale_log2 = scale * 1.4426950408889634f;
     a.q_heads = q_heads; a.group = q_heads / c.heads; a.causal = causal;
     const AttentionPlan p = attention_plan(B, max_new, max_kv, q_heads, c.heads, c.head_dim);
-    a.splits = p.splits;
-    a.chunk = (int)((max_kv + a.splits - 1) / a.splits + STEP - 1) / STEP * STEP;
     a.part_o = workspace;
-    a.part_ml = workspace + (p.prompt ? T * q_heads * p.part_rows : p.part_rows) * c.head_dim;
-    a.part_job = reinterpret_cast<int4*>(a.part_ml + p.part_rows * 4);     // few rows only
+    a.part_ml = workspace + p.part_rows * c.head_dim;
+    a.part_job = reinterpret_cast<int4*>(a.part_ml + p.part_rows * 4);
     a.tiles = (int)row_tiles(max_new, a.group);
     a.items = (int)(B * a.tiles);
     const dim3 grid((unsigned)p.blocks), join((unsigned)p.join_blocks);
@@ -954,25 +1048,21 @@ hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const 
         if (c.head_dim == 64) { if (one) go(Size<64>{}, std::true_type{}); else go(Size<64>{}, std::false_type{}); }
         else { if (one) go(Size<128>{}, std::true_type{}); else go(Size<128>{}, std::false_type{}); }
     };
-    if (p.prompt) {
-        with_sizes([&](auto d, auto one) {
-            hipLaunchKernelGGL((kv8_prompt_kernel<decltype(d)::value, decltype(one)::value>), grid, dim3(64 * P_WAVES), 0,
-                               stream, a);
-        });
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess || p.join_blocks == 0) return e;
-        if (c.head_dim == 64) hipLaunchKernelGGL(kv8_join_kernel<64>, join, dim3(64), 0, stream, a);
-        else hipLaunchKernelGGL(kv8_join_kernel<128>, join, dim3(64), 0, stream, a);
-        return hipGetLastError();
-    }
     with_sizes([&](auto d, auto one) {
-        hipLaunchKernelGGL((kv8_attention_kernel<decltype(d)::value, decltype(one)::value>), grid, dim3(64 * WAVES), 0,
-                           stream, a);
+        constexpr int D = decltype(d)::value;
+        constexpr bool ONE = decltype(one)::value;
+        if (p.prompt && p.deal) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, true>), grid, dim3(64 * P_WAVES), 0, stream, a);
+        else if (p.prompt) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, false>), grid, dim3(64 * P_WAVES), 0, stream, a);
+        else if (p.deal) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, true>), grid, dim3(64 * WAVES), 0, stream, a);
+        else hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false>), grid, dim3(64 * WAVES), 0, stream, a);
     });
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (c.head_dim == 64) hipLaunchKernelGGL(kv8_join_steps_kernel<64>, join, dim3(64 * WAVES), 0, stream, a);
-    else hipLaunchKernelGGL(kv8_join_steps_kernel<128>, join, dim3(64 * WAVES), 0, stream, a);
+    if (e != hipSuccess || !p.deal) return e;
+    with_sizes([&](auto d, auto) {
+        constexpr int D = decltype(d)::value;
+        if (p.prompt) hipLaunchKernelGGL((kv8_join_kernel<D, P_ROWS, TILE>), join, dim3(64 * WAVES), 0, stream, a);
+        else hipLaunchKernelGGL((kv8_join_kernel<D, ROWS, STEP>), join, dim3(64 * WAVES), 0, stream, a);
+    });
     return hipGetLastError();
 }
 

@@ -7,12 +7,12 @@
 namespace w4a8 {
 
 struct AttentionPlan {
-    bool prompt;              // many query rows a sequence: blocks of 256 rows, else of 16
-    int splits;               // of the context (many rows)
+    bool prompt;              // many query rows a sequence: blocks of 128 rows, else of 16
+    bool deal;                // equal shares of all steps, parts joined afterwards
     int64_t blocks, join_blocks;
-    int64_t part_rows;        // rows of partial results (many rows: for each row of q)
+    int64_t part_rows;        // rows of partial results
 };
 AttentionPlan attention_plan(int64_t B, int64_t max_new, int64_t max_kv, int q_heads, int kv_heads, int head_dim);
-int64_t attention_workspace(const AttentionPlan& p, int64_t T, int q_heads, int head_dim);
+int64_t attention_workspace(const AttentionPlan& p, int head_dim);
 
 }  // namespace w4a8
