@@ -25,7 +25,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import w4a8
-from .w4a8 import ROT_BLOCK, _check, _dev, _out, _stream
+from .w4a8 import ROT_BLOCK, _check, _dev, _out
 
 ABI_VERSION = 1
 NORM_MAX_K, ROPE_MAX_AXES, ROPE_MAX_HEAD_DIM = 16384, 4, 256
@@ -81,6 +81,11 @@ def call(fn: str, *args) -> int:
     return getattr(load(), fn)(*args)
 
 
+def _stream(t: torch.Tensor) -> int:
+    """The current stream's handle; without building a torch Stream object, which costs as much as half a launch."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -96,7 +101,7 @@ def _heads(x: torch.Tensor, name: str, heads: Optional[int] = None, head_dim: Op
     """Checks a bf16 [tokens, heads, head_dim] tensor with dense heads; its token stride."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor")
-    if x.dtype != torch.bfloat16 or x.dim() != 3:
+    if x.dtype is not torch.bfloat16 or x.dim() != 3:
         raise ValueError(f"{name} must be bfloat16 [tokens, heads, head_dim]")
     t, h, d = x.shape
     if (heads is not None and h != heads) or (head_dim is not None and d != head_dim) or (rows is not None and t != rows):
@@ -121,8 +126,7 @@ def _weight(weight: torch.Tensor, k: int) -> None:
         raise ValueError(f"weight must have shape ({k},), got {tuple(weight.shape)}")
 
 
-def _norm(x, weight, residual, eps, qmax, h, rstd, y, xq, xs):
-    m, k = _rows(x, "x")
+def _norm(m, k, x, weight, residual, eps, qmax, h, rstd, y, xq, xs):
     _weight(weight, k)
     stream = torch.bfloat16
     if residual is not None:
@@ -153,14 +157,14 @@ def rmsnorm_quant_act(x, weight, residual=None, eps: float = 1e-6, qmax: int = 1
     xs = _out(xs, (m,), torch.float32, x.device, "xs")
     if y is not None:
         _out(y, (m, k), torch.bfloat16, x.device, "y")
-    return xq, xs, _norm(x, weight, residual, eps, qmax, h, rstd, y, xq, xs)
+    return xq, xs, _norm(m, k, x, weight, residual, eps, qmax, h, rstd, y, xq, xs)
 
 
 def rmsnorm(x, weight, residual=None, eps: float = 1e-6, h=None, rstd=None, y=None):
     """The same norm without the int8 rows (a final norm): (y bf16 [M, K], h)."""
     m, k = _rows(x, "x")
     y = _out(y, (m, k), torch.bfloat16, x.device, "y")
-    return y, _norm(x, weight, residual, eps, 127, h, rstd, y, None, None)
+    return y, _norm(m, k, x, weight, residual, eps, 127, h, rstd, y, None, None)
 
 
 def rmsnorm_grad(grad, h, rstd, weight, grad_h=None, rotated: bool = True, dx=None, dweight=None,

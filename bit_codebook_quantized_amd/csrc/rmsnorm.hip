@@ -156,20 +156,32 @@ __global__ __launch_bounds__(1024) void rmsnorm_grad_kernel(const uint16_t* __re
     if (partial) store16(partial + ((int64_t)blockIdx.x * rows + pl.row_local) * K + col, dw);
 }
 
-// dweight[k] = sum over the partial rows, 16 columns a block, 16 lanes down the rows each.
-__global__ __launch_bounds__(256) void rmsnorm_dweight_kernel(const float* __restrict__ partial, int rows, int K,
-                                                              float* __restrict__ dweight) {
-    __shared__ float sm[256];
-    const int tid = threadIdx.x, c = tid & 15, p = tid >> 4;
-    const int col = blockIdx.x * 16 + c;
-    float a = 0.0f;
-    for (int r = p; r < rows; r += 16) a += partial[(int64_t)r * K + col];
-    sm[tid] = a;
-    __syncthreads();
-    if (p == 0) {
-        for (int j = 1; j < 16; ++j) a += sm[16 * j + c];
-        dweight[col] = a;
+// dweight[k] = sum over the partial rows: 64 columns a block, 4 a lane (256-byte row pieces), 64
+// lanes down the rows, then their sums through LDS, each in a fixed order.
+constexpr int DW_THREADS = 1024;
+__global__ __launch_bounds__(DW_THREADS) void rmsnorm_dweight_kernel(const float* __restrict__ partial, int rows, int K,
+                                                                     float* __restrict__ dweight) {
+    __shared__ __attribute__((aligned(16))) float4 sm[64][16];
+    const int c = threadIdx.x & 15, p = threadIdx.x >> 4;
+    const float4* src = reinterpret_cast<const float4*>(partial + blockIdx.x * 64) + c;
+    const int64_t stride = K / 4;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int r = p; r < rows; r += 64) {
+        const float4 v = src[r * stride];
+        a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
     }
+    sm[p][c] = a;
+#pragma unroll
+    for (int half = 32; half > 0; half >>= 1) {
+        __syncthreads();
+        if (p < half) {
+            const float4 v = sm[p + half][c];
+            a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+            sm[p][c] = a;
+        }
+    }
+    if (p == 0) reinterpret_cast<float4*>(dweight + blockIdx.x * 64)[c] = a;
 }
 
 size_t norm_lds(int nb) { return (128 + (size_t)norm_slots(nb) * NT_SLOT) * sizeof(float); }
@@ -236,7 +248,7 @@ hipError_t launch_rmsnorm_grad(const void* grad, const void* h, int stream_f32, 
         if (e != hipSuccess) return e;
     }
     if (dweight)
-        hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3(K / 16), dim3(256), 0, stream, partial,
+        hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3(K / 64), dim3(DW_THREADS), 0, stream, partial,
                            (int)rmsnorm_grad_partial_rows(M, K), K, dweight);
     return hipGetLastError();
 }

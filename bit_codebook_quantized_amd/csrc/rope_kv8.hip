@@ -225,16 +225,17 @@ __device__ __forceinline__ PageScale page_scale(uint32_t top, const float* store
     return s;
 }
 
-constexpr int APPEND_ITEMS = 4;     // pieces of 16 elements a thread, at most 128 tokens x 128 / 256 threads
+// NI: pieces of 16 elements a thread, page_tokens * head_dim / (16 * 256 threads) of them at most.
 
 // Keys: a thread's pieces stay in registers between the page's maximum and the codes.
+template <int NI>
 __device__ void append_keys(const AppendArgs& a, const RopeArgs& r, const PageJob& job, int head, uint32_t* sm) {
     const int D = a.c.head_dim, P = a.c.page_tokens, pieces = D >> 4;
     const int n = (job.j1 - job.j0) * pieces;
-    float lo[APPEND_ITEMS][8], hi[APPEND_ITEMS][8];
+    float lo[NI][8], hi[NI][8];
     uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < APPEND_ITEMS; ++e) {
+    for (int e = 0; e < NI; ++e) {
         const int i = threadIdx.x + e * ROPE_THREADS;
         if (i < n) {
             const int t = i / pieces;
@@ -258,7 +259,7 @@ __device__ void append_keys(const AppendArgs& a, const RopeArgs& r, const PageJo
     __syncthreads();                       // every thread has read the old scale
     if (threadIdx.x == 0) a.c.k_scale[ph] = s.now;
 #pragma unroll
-    for (int e = 0; e < APPEND_ITEMS; ++e) {
+    for (int e = 0; e < NI; ++e) {
         const int i = threadIdx.x + e * ROPE_THREADS;
         if (i < n) {
             const int t = i / pieces;
@@ -285,13 +286,14 @@ constexpr int VT_STRIDE = 128 + 16;        // bytes of a value row (tokens) in L
 
 // Values: the codes go through LDS into token order, so a page row is written 16 tokens at
 // a time.
+template <int NI>
 __device__ void append_values(const AppendArgs& a, const PageJob& job, int head, uint32_t* sm, uint8_t* vt) {
     const int D = a.c.head_dim, P = a.c.page_tokens, pieces = D >> 4;
     const int n = (job.j1 - job.j0) * pieces;
-    float lo[APPEND_ITEMS][8], hi[APPEND_ITEMS][8];
+    float lo[NI][8], hi[NI][8];
     uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < APPEND_ITEMS; ++e) {
+    for (int e = 0; e < NI; ++e) {
         const int i = threadIdx.x + e * ROPE_THREADS;
         if (i < n) {
             const int t = i / pieces, c = i - t * pieces;
@@ -307,7 +309,7 @@ __device__ void append_values(const AppendArgs& a, const PageJob& job, int head,
     top = block_top(top, sm);
     const PageScale s = page_scale(top, a.c.v_scale + ph, job.j0 > 0);
 #pragma unroll
-    for (int e = 0; e < APPEND_ITEMS; ++e) {
+    for (int e = 0; e < NI; ++e) {
         const int i = threadIdx.x + e * ROPE_THREADS;
         if (i < n) {
             const int t = i / pieces, c = i - t * pieces;
@@ -352,6 +354,7 @@ __device__ void append_values(const AppendArgs& a, const PageJob& job, int head,
 
 // Blocks below cache_blocks each own one page of one sequence, one head, and its keys or its
 // values, so nothing is shared between blocks; the rest rotate the queries.
+template <int NI>
 __global__ __launch_bounds__(ROPE_THREADS) void kv8_append_kernel(AppendArgs a, RopeArgs r, RopeRun q) {
     __shared__ __attribute__((aligned(16))) uint8_t vt[128 * VT_STRIDE];
     __shared__ uint32_t sm[4];
@@ -367,8 +370,8 @@ __global__ __launch_bounds__(ROPE_THREADS) void kv8_append_kernel(AppendArgs a, 
     block /= a.c.heads;
     const PageJob job = page_job(a, block / a.pages_per_seq, (int)(block % a.pages_per_seq));
     if (job.page < 0) return;
-    if (values) append_values(a, job, head, sm, vt);
-    else append_keys(a, r, job, head, sm);
+    if (values) append_values<NI>(a, job, head, sm, vt);
+    else append_keys<NI>(a, r, job, head, sm);
 }
 static_assert(2 * ROPE_LDS_PAIRS * sizeof(float) <= 128 * VT_STRIDE, "cos and sin fit in the value buffer");
 
@@ -448,7 +451,11 @@ hipError_t launch_append(const w4a8_kv8& c, const int32_t* ctx_len, const int32_
         blocks += rope_blocks(run);
     }
     if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL(kv8_append_kernel, dim3((unsigned)blocks), dim3(ROPE_THREADS), 0, stream, a, r, run);
+    const int pieces = c.page_tokens * c.head_dim / (16 * ROPE_THREADS);
+    const dim3 grid((unsigned)blocks), threads(ROPE_THREADS);
+    if (pieces <= 1) hipLaunchKernelGGL(kv8_append_kernel<1>, grid, threads, 0, stream, a, r, run);
+    else if (pieces <= 2) hipLaunchKernelGGL(kv8_append_kernel<2>, grid, threads, 0, stream, a, r, run);
+    else hipLaunchKernelGGL(kv8_append_kernel<4>, grid, threads, 0, stream, a, r, run);
     return hipGetLastError();
 }
 
