@@ -55,6 +55,7 @@ struct AttArgs {
     int4* part_job;       // [blocks]: item (-1: nothing to join), head, last block, first slot
     float scale_log2;     // scale * log2(e)
     int q_heads, group, causal;
+    int chunk_steps, chunks;   // many query rows: steps of a chunk of the context, most chunks
     int tiles, items;     // row tiles of a sequence with max_new tokens; of all sequences
 };
 
@@ -317,7 +318,10 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l) - W_EXP) * 0.69314718055994531f;
 }
 
-// How the work is dealt.  It is a list of steps: for every sequence, row tile (R rows) and
+// Many query rows: from this many rows of a sequence on; waves, 16-row tiles a wave, rows of a block.
+constexpr int PROMPT_ROWS = 128, P_WAVES = 4, P_QT = 2, P_ROWS = 16 * P_QT * P_WAVES;
+
+// How the work of few query rows is dealt.  It is a list of steps: for every sequence, row tile (R rows) and
 // head, the steps of S keys that its rows see.  The list is dealt to the blocks in equal
 // contiguous shares, whatever the sequences' lengths are, so a block holds pieces of a few
 // (row tile, head) pairs; a piece that is not all of one leaves its part in the workspace
@@ -663,22 +667,48 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv8_attention_kernel(AttArgs a)
     } while (DEAL && next_piece(a, walks[wave], piece, x));
 }
 
-// Joins the parts of the row tile and head that one block of the main launch began, 16 rows a
-// block: the waves take parts in turn with a running maximum, then join through LDS.  A lane has
-// 4 columns of every 64 / (D / 4)-th row.
-template <int D, int R, int S>
+// First part row of a (row tile, head) pair's chunk (many query rows).
+__device__ __forceinline__ int64_t part_slot(const AttArgs& a, int index, int head, int chunk) {
+    return (((int64_t)index * a.c.heads + head) * a.chunks + chunk) * P_ROWS;
+}
+
+// Joins the parts of one (row tile, head) pair, 16 rows a block: the waves take parts in turn
+// with a running maximum, then join through LDS.  A lane has 4 columns of every 64 / (D / 4)-th
+// row.  Few query rows: the pair that block blockIdx.x of the main launch began.  Many: the
+// pair's chunks.
+template <int D, bool MANY>
 __global__ __launch_bounds__(64 * WAVES) void kv8_join_kernel(AttArgs a) {
     constexpr int LANES = D / 4, AT_ONCE = 64 / LANES, NR = ROWS / AT_ONCE;
     __shared__ __attribute__((aligned(16))) float so[WAVES][ROWS][D];
     __shared__ float sm[WAVES][ROWS], sl[WAVES][ROWS], slo[WAVES][ROWS];
-    const int first = blockIdx.x / (R / ROWS), sub0 = blockIdx.x % (R / ROWS) * ROWS;
-    const int4 job = a.part_job[first];
-    if (job.x < 0) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int sub = lane / LANES, col = 4 * (lane % LANES);
-    const Item x = one_item<R, S>(a, uniform(job.x));
-    const int count = min(ROWS, x.rows - x.row0 - sub0), last = job.z;
-    if (count <= 0) return;
+    int head, count, row0, parts;
+    int64_t q0, slot0, slot1;       // slots of the first part and of the second; the others follow it
+    constexpr int64_t NEXT = MANY ? P_ROWS : 2 * ROWS;
+    if constexpr (MANY) {
+        const int pair = blockIdx.x / (P_ROWS / ROWS), sub0 = blockIdx.x % (P_ROWS / ROWS) * ROWS;
+        head = pair % a.c.heads;
+        const Item x = one_item<P_ROWS, TILE>(a, pair / a.c.heads);
+        parts = min(a.chunks, (x.steps + a.chunk_steps - 1) / a.chunk_steps);
+        row0 = x.row0 + sub0;
+        count = min(ROWS, x.rows - row0);
+        if (parts < 2 || count <= 0) return;
+        q0 = x.s.q0;
+        slot0 = part_slot(a, pair / a.c.heads, head, 0) + sub0;
+        slot1 = slot0 + NEXT;
+    } else {
+        const int4 job = a.part_job[blockIdx.x];
+        if (job.x < 0) return;
+        const Item x = one_item<ROWS, STEP>(a, uniform(job.x));
+        head = job.y;
+        row0 = x.row0;
+        count = min(ROWS, x.rows - row0);
+        q0 = x.s.q0;
+        parts = job.z - (int)blockIdx.x + 1;
+        slot0 = (2 * (int64_t)blockIdx.x + job.w) * ROWS;
+        slot1 = 2 * ((int64_t)blockIdx.x + 1) * ROWS;
+    }
 
     f32x4 v[NR];
     float m[NR], l[NR], lo[NR];
@@ -688,8 +718,8 @@ __global__ __launch_bounds__(64 * WAVES) void kv8_join_kernel(AttArgs a) {
         m[j] = -__builtin_inff();
         l[j] = lo[j] = 0.0f;
     }
-    for (int i = first + wave; i <= last; i += WAVES) {
-        const int64_t slot = (2 * (int64_t)i + (i == first ? job.w : 0)) * R + sub0;
+    for (int i = wave; i < parts; i += WAVES) {
+        const int64_t slot = i == 0 ? slot0 : slot1 + (i - 1) * NEXT;
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
             const int r = AT_ONCE * j + sub;
@@ -730,8 +760,8 @@ __global__ __launch_bounds__(64 * WAVES) void kv8_join_kernel(AttArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(p[e], f, y[e]);
         }
-        const int64_t t = x.s.q0 + (x.row0 + sub0 + r) / a.group;
-        const int qh = job.y * a.group + (x.row0 + sub0 + r) % a.group;
+        const int64_t t = q0 + (row0 + r) / a.group;
+        const int qh = head * a.group + (row0 + r) % a.group;
         const float inv = 1.0f / lot;
         *reinterpret_cast<uint2*>(a.out + t * a.out_stride + (int64_t)qh * D + d) =
             lt == 0.0f ? make_uint2(0, 0) : make_uint2(f32x2_to_bf16x2(y[0] * inv, y[1] * inv), f32x2_to_bf16x2(y[2] * inv, y[3] * inv));
@@ -758,12 +788,11 @@ __device__ __forceinline__ int lds_piece(int r, int p) {
 // slower on prompts of 2000).  The loop is near three limits at once, matrix instructions, LDS
 // reads and vector instructions (about 2100, 2300 and 2800 cycles a tile and CU); reads
 // are issued four ahead of the products that use them, which the compiler does not do itself.
-constexpr int PROMPT_ROWS = 128;     // from this many rows of a sequence on
-constexpr int P_WAVES = 4, P_QT = 2, P_ROWS = 16 * P_QT * P_WAVES;
 
-template <int D, bool ONE_PAGE, bool DEAL>
+template <int D, bool ONE_PAGE, bool SPLIT>
 __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) {
     constexpr int NS = D / 32, NV = D / 16;
+    constexpr int AHEAD = 4;         // fragments read before the product that uses the first
     constexpr int CHUNKS = TILE * D / 16;                   // 16-code pieces of a tile's keys, or values
     __shared__ __attribute__((aligned(16))) uint16_t sk[2][TILE * D];
     __shared__ __attribute__((aligned(16))) uint16_t sv[2][D * TILE];
@@ -771,25 +800,25 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
     const int wave = uniform((int)threadIdx.x >> 6);
     const int shift = 31 - __clz(a.c.page_tokens), in_page = a.c.page_tokens - 1;
     const bool want_lse = a.lse != nullptr;
-    __shared__ Walk<P_ROWS, TILE> walks[P_WAVES];
-    Piece job;
-    Item x;
-    if constexpr (DEAL) {
-        if (threadIdx.x == 0) a.part_job[blockIdx.x] = make_int4(-1, 0, 0, 0);
-        Walk<P_ROWS, TILE> walk;
-        if (!walk.begin(a, threadIdx.x & 63) || !walk.next(a, job, x)) return;
-        walk.keep(walks[wave]);
-    } else if (!own_item<P_ROWS, TILE>(a, job, x)) {
-        return;
-    }
-    do {
-    const int tid = DEAL ? anew(threadIdx.x) : threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
-    const int head = job.head;
+    // heads fastest, then the context's chunks, then the row tiles of a sequence, the last ones
+    // first (causal rows see more the later they are)
+    int id = blockIdx.x;
+    const int head = id % a.c.heads;
+    id /= a.c.heads;
+    const int chunk = SPLIT ? id % a.chunks : 0;
+    if (SPLIT) id /= a.chunks;
+    const int index = id / a.tiles * a.tiles + a.tiles - 1 - id % a.tiles;
+    const Item x = one_item<P_ROWS, TILE>(a, index);
+    const int step = SPLIT ? chunk * a.chunk_steps : 0, left = x.steps - step;
+    const int steps = SPLIT && chunk < a.chunks - 1 ? min(left, a.chunk_steps) : left;
+    if (steps <= 0) return;
+    const bool all = !SPLIT || steps == x.steps;
+    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
     const Seq& s = x.s;
     const Span& span = x.span;
     const int rows = x.rows, row0 = x.row0;
-    const int32_t* const table = a.c.table + (int64_t)(job.index / a.tiles) * a.c.table_stride;
-    const int k0 = (span.low / TILE + job.step) * TILE, k1 = min(span.top, k0 + job.steps * TILE);
+    const int32_t* const table = a.c.table + (int64_t)(index / a.tiles) * a.c.table_stride;
+    const int k0 = (span.low / TILE + step) * TILE, k1 = min(span.top, k0 + steps * TILE);
 
     // this wave's rows
     const int wrow0 = row0 + 16 * P_QT * wave;
@@ -886,13 +915,13 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
 #pragma unroll
                 for (int t = 0; t < P_QT; ++t) o[t][i] = mfma(v, e ? w[t].hi : w[t].lo, o[t][i]);
             }
-        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
 #pragma unroll
-        for (int i = 0; i < 2 * NV - 4; ++i) {
+        for (int i = 0; i < 2 * NV - AHEAD; ++i) {
             __builtin_amdgcn_sched_group_barrier(0x008, P_QT, 0);
             __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
-        __builtin_amdgcn_sched_group_barrier(0x008, 4 * P_QT, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, AHEAD * P_QT, 0);
     };
 
     if (k0 < k1) {
@@ -928,13 +957,13 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
                     for (int t = 0; t < P_QT; ++t) acc[t][j] = mfma(k, qf[t][i], acc[t][j]);
                 }
             }
-            __builtin_amdgcn_sched_group_barrier(0x100, 4, 1);
+            __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 1);
 #pragma unroll
-            for (int i = 0; i < 4 * NS - 4; ++i) {
+            for (int i = 0; i < 4 * NS - AHEAD; ++i) {
                 __builtin_amdgcn_sched_group_barrier(0x008, P_QT, 1);
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
             }
-            __builtin_amdgcn_sched_group_barrier(0x008, 4 * P_QT, 1);
+            __builtin_amdgcn_sched_group_barrier(0x008, AHEAD * P_QT, 1);
             const bool plain = whole && kt + TILE <= wspan.common && kt >= wspan.high && plain_tile(info);
             if (plain) {
 #pragma unroll
@@ -958,7 +987,7 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
         if (wrow0 + 16 * t + c >= rows) continue;
         const Row mine = row_of(a, s, head, wrow0 + 16 * t + c, rows);
         const int64_t tok = s.q0 + mine.token;
-        if (!DEAL || job.whole) {
+        if (all) {
             const float inv = l == 0.0f ? 0.0f : vtop / lo;
             uint16_t* dst = a.out + tok * a.out_stride + (int64_t)mine.head * D + 4 * g;
 #pragma unroll
@@ -969,15 +998,13 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
             }
             if (want_lse && g == 0) a.lse[tok * a.q_heads + mine.head] = lse_of(st[t].m, l);
         } else {
-            const int64_t slot = job.slot + 16 * (P_QT * wave + t) + c;
+            const int64_t slot = part_slot(a, index, head, chunk) + 16 * (P_QT * wave + t) + c;
             float* dst = a.part_o + slot * D + 4 * g;
 #pragma unroll
             for (int i = 0; i < NV; ++i) *reinterpret_cast<f32x4*>(dst + 16 * i) = o[t][i] * vtop;
             if (g == 0) *reinterpret_cast<float4*>(a.part_ml + slot * 4) = make_float4(st[t].m, l, lo, 0.0f);
         }
     }
-    __syncthreads();       // the tiles in LDS are free again
-    } while (DEAL && next_piece(a, walks[wave], job, x));
 }
 
 // Rows of a block: 128 where a sequence has that many, else 16 (the keys are then split over
@@ -993,32 +1020,42 @@ int64_t row_tiles(int64_t max_new, int group) {
 
 }  // namespace
 
-// Blocks of a launch: one for each (row tile, head), or 512 (two a CU, as many as fit at once)
-// that share all steps equally and whose parts are then joined.  Dealing costs the parts'
-// traffic and a second launch, and pays where the pairs leave blocks idle for long: measured
-// with 128 rows, by about ten steps of 64 keys (1 x 500 of 500 tokens, 32 heads: 29 us a
-// block each, 46 us dealt; 4 x 300 of 2048: 98 and 72 us; 4 x 128 of 8192: 153 and 87 us).
-// With few rows a step is 256 keys, and lengths are uneven as a rule, so long contexts are
-// dealt however many pairs there are (16 x up to 32 k tokens: 181 us in fixed splits, 115
-// dealt; 256 x up to 400: 57 us dealt, 34 us a block each).  There are never
-// more blocks than steps (few rows) or a quarter of that (128 rows).
+// Blocks of a launch.
+// Few rows (a step is 256 keys): one for each (row tile, head), or 512 (two a CU, as many as fit
+// at once) that share all steps equally and whose parts are then joined.  Dealing costs a second
+// launch and pays where pairs would leave blocks idle, by three steps; lengths are uneven as a
+// rule, so contexts of eight steps are dealt however many pairs there are (16 x up to 32 k
+// tokens: 181 us in fixed splits, 115 dealt; 256 x up to 400: 57 us dealt, 34 us a block each).
+// Many rows (a step is 64 keys): one for each pair, or, where that is less than 512, for each
+// chunk of a pair's context, about 1024 in all and no less than six steps a chunk.
 AttentionPlan attention_plan(int64_t B, int64_t max_new, int64_t max_kv, int q_heads, int kv_heads, int head_dim) {
     const int group = q_heads / kv_heads;
     AttentionPlan p{};
     p.prompt = is_prompt(max_new, group);
-    const int64_t base = B * kv_heads * row_tiles(max_new, group), rows = p.prompt ? P_ROWS : ROWS;
-    const int64_t steps = std::max<int64_t>(1, p.prompt ? max_kv / TILE : (max_kv + STEP - 1) / STEP);
-    const int64_t idle = steps * std::max<int64_t>(0, DEAL_BLOCKS - base);      // in steps of all blocks
-    p.deal = p.prompt ? idle >= 10 * DEAL_BLOCKS : steps >= 8 || idle >= 3 * DEAL_BLOCKS;
-    p.blocks = p.deal ? std::min<int64_t>(DEAL_BLOCKS, base * (p.prompt ? (steps + 3) / 4 : steps)) : base;
-    p.join_blocks = p.deal ? p.blocks * (rows / ROWS) : 0;
-    p.part_rows = p.deal ? p.blocks * 2 * rows : 0;
+    const int64_t base = B * kv_heads * row_tiles(max_new, group);
+    if (p.prompt) {
+        const int64_t steps = std::max<int64_t>(1, (max_kv + TILE - 1) / TILE);
+        const int64_t chunk = std::max<int64_t>(6, (base * steps + 2 * DEAL_BLOCKS - 1) / (2 * DEAL_BLOCKS));
+        p.parts = base < DEAL_BLOCKS && 2 * steps > 3 * chunk;
+        // a context longer than max_kv is still walked: its last chunk is the longest
+        p.chunks = p.parts ? (int)((steps + chunk - 1) / chunk) : 1;
+        p.chunk_steps = (int)chunk;
+        p.blocks = base * p.chunks;
+        p.join_blocks = p.parts ? base * (P_ROWS / ROWS) : 0;
+        p.part_rows = p.parts ? base * p.chunks * P_ROWS : 0;
+        return p;
+    }
+    const int64_t steps = std::max<int64_t>(1, (max_kv + STEP - 1) / STEP);
+    p.parts = steps >= 8 || steps * std::max<int64_t>(0, DEAL_BLOCKS - base) >= 3 * DEAL_BLOCKS;
+    p.blocks = p.parts ? std::min<int64_t>(DEAL_BLOCKS, base * steps) : base;
+    p.join_blocks = p.parts ? p.blocks : 0;
+    p.part_rows = p.parts ? p.blocks * 2 * ROWS : 0;
     return p;
 }
 
 // Floats of workspace.
 int64_t attention_workspace(const AttentionPlan& p, int head_dim) {
-    return p.deal ? p.part_rows * (head_dim + 4) + 4 * p.blocks : 0;
+    return p.parts ? p.part_rows * (head_dim + 4) + (p.prompt ? 0 : 4 * p.blocks) : 0;
 }
 
 hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const w4a8_kv8& c, const int32_t* kv_len,
@@ -1039,6 +1076,8 @@ hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const 
     a.part_o = workspace;
     a.part_ml = workspace + p.part_rows * c.head_dim;
     a.part_job = reinterpret_cast<int4*>(a.part_ml + p.part_rows * 4);
+    a.chunk_steps = p.chunk_steps;
+    a.chunks = p.chunks;
     a.tiles = (int)row_tiles(max_new, a.group);
     a.items = (int)(B * a.tiles);
     const dim3 grid((unsigned)p.blocks), join((unsigned)p.join_blocks);
@@ -1051,17 +1090,17 @@ hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const 
     with_sizes([&](auto d, auto one) {
         constexpr int D = decltype(d)::value;
         constexpr bool ONE = decltype(one)::value;
-        if (p.prompt && p.deal) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, true>), grid, dim3(64 * P_WAVES), 0, stream, a);
+        if (p.prompt && p.parts) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, true>), grid, dim3(64 * P_WAVES), 0, stream, a);
         else if (p.prompt) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, false>), grid, dim3(64 * P_WAVES), 0, stream, a);
-        else if (p.deal) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, true>), grid, dim3(64 * WAVES), 0, stream, a);
+        else if (p.parts) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, true>), grid, dim3(64 * WAVES), 0, stream, a);
         else hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false>), grid, dim3(64 * WAVES), 0, stream, a);
     });
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !p.deal) return e;
+    if (e != hipSuccess || !p.parts) return e;
     with_sizes([&](auto d, auto) {
         constexpr int D = decltype(d)::value;
-        if (p.prompt) hipLaunchKernelGGL((kv8_join_kernel<D, P_ROWS, TILE>), join, dim3(64 * WAVES), 0, stream, a);
-        else hipLaunchKernelGGL((kv8_join_kernel<D, ROWS, STEP>), join, dim3(64 * WAVES), 0, stream, a);
+        if (p.prompt) hipLaunchKernelGGL((kv8_join_kernel<D, true>), join, dim3(64 * WAVES), 0, stream, a);
+        else hipLaunchKernelGGL((kv8_join_kernel<D, false>), join, dim3(64 * WAVES), 0, stream, a);
     });
     return hipGetLastError();
 }

@@ -8,7 +8,8 @@ namespace w4a8 {
 
 struct AttentionPlan {
     bool prompt;              // many query rows a sequence: blocks of 128 rows, else of 16
-    bool deal;                // equal shares of all steps, parts joined afterwards
+    bool parts;               // blocks leave partial results, joined by a second launch
+    int chunks, chunk_steps;  // many rows: most chunks of a context, steps of 64 keys in one
     int64_t blocks, join_blocks;
     int64_t part_rows;        // rows of partial results
 };
