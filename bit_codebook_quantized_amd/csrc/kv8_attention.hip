@@ -36,7 +36,6 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int TILE = 64;             // keys of a step
-constexpr int ROWS = 16;             // query rows of a block
 constexpr int WAVES = 4;             // waves of a block: they share the rows and split the keys
 constexpr int STEP = TILE * WAVES;   // keys of a block's step
 constexpr float W_EXP = 15.0f;       // weights are kept times 2^15
@@ -291,7 +290,8 @@ __device__ __forceinline__ Span span_of(const AttArgs& a, const Seq& s, int row0
     return p;
 }
 
-// One query row: its place in q and out, and the keys it sees.
+// One query row: its place in q and out, and the keys it sees.  Lanes past a sequence's last row
+// repeat it (and store nothing), so that they need no care.
 struct Row {
     int token, head, begin, end;
 };
@@ -303,7 +303,6 @@ __device__ __forceinline__ Row row_of(const AttArgs& a, const Seq& s, int kv_hea
     const int pos = s.pos0 + x.token;
     x.end = a.causal && pos + 1 < s.len ? pos + 1 : s.len;
     x.begin = a.window > 0 && pos - a.window + 1 > 0 ? (int)(pos - a.window + 1) : 0;
-    if (row >= rows) x.end = 0;
     return x;
 }
 
@@ -512,24 +511,25 @@ __device__ __forceinline__ bool own_item(const AttArgs& a, Piece& p, Item& x) {
 // A wave loads its tile straight into registers in the order of the matrix operands: the
 // values of a tile while its scores are made, the keys of the next one while its weights are
 // used.  The four waves take the step's four tiles and are joined through LDS.
-template <int D, bool ONE_PAGE, bool DEAL>
-__global__ __launch_bounds__(64 * WAVES, 2) void kv8_attention_kernel(AttArgs a) {
+template <int D, bool ONE_PAGE, bool DEAL, int QT>
+__global__ __launch_bounds__(64 * WAVES, QT == 1 ? 2 : 1) void kv8_attention_kernel(AttArgs a) {
     constexpr int NK = D / 64;       // 16-byte key loads a lane and sub-tile
     constexpr int NV = D / 16;       // value column tiles
-    // the waves' results: O^T [wave][D][16 + 1], maxima and sums
-    __shared__ float so[WAVES][D][ROWS + 1];
-    __shared__ float sm[WAVES][ROWS], sl[WAVES][ROWS], slo[WAVES][ROWS];
+    constexpr int R = 16 * QT;       // rows of a block
+    // the waves' results, 16 rows at a time: O^T [wave][D][16 + 1], maxima and sums
+    __shared__ float so[WAVES][D][16 + 1];
+    __shared__ float sm[WAVES][16], sl[WAVES][16], slo[WAVES][16];
 
-    __shared__ Walk<ROWS, STEP> walks[WAVES];
+    __shared__ Walk<R, STEP> walks[WAVES];
     const int wave = uniform((int)threadIdx.x >> 6);
     Piece piece;
     Item x;
     if constexpr (DEAL) {
         if (threadIdx.x == 0) a.part_job[blockIdx.x] = make_int4(-1, 0, 0, 0);
-        Walk<ROWS, STEP> walk;
+        Walk<R, STEP> walk;
         if (!walk.begin(a, threadIdx.x & 63) || !walk.next(a, piece, x)) return;
         walk.keep(walks[wave]);
-    } else if (!own_item<ROWS, STEP>(a, piece, x)) {
+    } else if (!own_item<R, STEP>(a, piece, x)) {
         return;
     }
     const int shift = 31 - __clz(a.c.page_tokens), in_page = a.c.page_tokens - 1;
@@ -542,24 +542,24 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv8_attention_kernel(AttArgs a)
         const Span& span = x.span;
         const int rows = x.rows, row0 = x.row0;
         const int32_t* const table = a.c.table + (int64_t)(piece.index / a.tiles) * a.c.table_stride;
-        const Row row = row_of(a, s, head, row0 + c, rows);
-        const bool whole = row0 + ROWS <= rows;
         const int first = (span.low / STEP + piece.step) * STEP;
         const int k0 = first + wave * TILE, k1 = min(span.top, first + piece.steps * STEP);
 
-        bf16x8 qf[2 * NK];
-        {
-            const uint16_t* src = a.q + (s.q0 + row.token) * a.q_stride + (int64_t)row.head * D;
+        Row row[QT];
+        bf16x8 qf[QT][2 * NK];
+        RowState st[QT];
+        f32x4 o[QT][NV];
 #pragma unroll
-            for (int i = 0; i < NK; ++i)
+        for (int q = 0; q < QT; ++q) {
+            row[q] = row_of(a, s, head, row0 + 16 * q + c, rows);
+            const uint16_t* src = a.q + (s.q0 + row[q].token) * a.q_stride + (int64_t)row[q].head * D + 16 * g;
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    qf[2 * i + e] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(src + 64 * i + 16 * g + 8 * e));
+            for (int i = 0; i < 2 * NK; ++i)
+                qf[q][i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(src + 64 * (i >> 1) + 8 * (i & 1)));
+            st[q] = fresh_row();
+#pragma unroll
+            for (int i = 0; i < NV; ++i) o[q][i] = f32x4{0, 0, 0, 0};
         }
-        RowState st = fresh_row();
-        f32x4 o[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) o[i] = f32x4{0, 0, 0, 0};
 
         // lane (c, g): keys from row c of a sub-tile (tokens 16 (c / 4) + 4 j + c % 4), 16 codes
         // of every 64; values of tokens 16 g .. 16 g + 15.  Page numbers are fetched a step
@@ -597,73 +597,87 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv8_attention_kernel(AttArgs a)
             const bool more = kt + STEP < k1;
             if (more) pages(kt + STEP);
 
-            f32x4 acc[4];
+            f32x4 acc[QT][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                acc[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int q = 0; q < QT; ++q) acc[q][j] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < NK; ++i) {
                     const uint4 w = kw[j * NK + i];
-                    acc[j] = mfma(widen(w.x, w.y), qf[2 * i], acc[j]);
-                    acc[j] = mfma(widen(w.z, w.w), qf[2 * i + 1], acc[j]);
+                    const bf16x8 lo = widen(w.x, w.y), hi = widen(w.z, w.w);
+#pragma unroll
+                    for (int q = 0; q < QT; ++q) acc[q][j] = mfma(lo, qf[q][2 * i], acc[q][j]);
+#pragma unroll
+                    for (int q = 0; q < QT; ++q) acc[q][j] = mfma(hi, qf[q][2 * i + 1], acc[q][j]);
                 }
             }
             if (more) load_keys(kt + STEP);
             const TileInfo t = tile_info<ONE_PAGE>(ks, vs, a.scale_log2, kt + 16 * g, present);
-            const bool plain = whole && kt + TILE <= span.common && kt >= span.high && plain_tile(t);
-            Weights w;
-            const float alpha = plain ? softmax_plain<ONE_PAGE>(acc, t, want_lse, st, w) : softmax_any(acc, t, row.begin, row.end, st, w);
-            if (__any(alpha != 1.0f)) {
+            const bool plain = kt + TILE <= span.common && kt >= span.high && plain_tile(t);
+            Weights w[QT];
 #pragma unroll
-                for (int i = 0; i < NV; ++i) o[i] *= alpha;
+            for (int q = 0; q < QT; ++q) {
+                const float alpha = plain ? softmax_plain<ONE_PAGE>(acc[q], t, want_lse, st[q], w[q])
+                                          : softmax_any(acc[q], t, row[q].begin, row[q].end, st[q], w[q]);
+                if (__any(alpha != 1.0f)) {
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) o[q][i] *= alpha;
+                }
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                o[i] = mfma(widen_f16(vw[i].x, vw[i].y), w.lo, o[i]);
-                o[i] = mfma(widen_f16(vw[i].z, vw[i].w), w.hi, o[i]);
+                const f16x8 lo = widen_f16(vw[i].x, vw[i].y), hi = widen_f16(vw[i].z, vw[i].w);
+#pragma unroll
+                for (int q = 0; q < QT; ++q) o[q][i] = mfma(lo, w[q].lo, o[q][i]);
+#pragma unroll
+                for (int q = 0; q < QT; ++q) o[q][i] = mfma(hi, w[q].hi, o[q][i]);
             }
         }
-        const float vtop = __builtin_amdgcn_exp2f(st.lv);
-        if (g == 0) { sm[wave][c] = st.m; sl[wave][c] = st.l; slo[wave][c] = st.lo; }
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int q = 0; q < QT; ++q) {
+            const float vtop = __builtin_amdgcn_exp2f(st[q].lv);
+            if (g == 0) { sm[wave][c] = st[q].m; sl[wave][c] = st[q].l; slo[wave][c] = st[q].lo; }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) so[wave][16 * i + 4 * g + e][c] = o[i][e] * vtop;
-        __syncthreads();
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) so[wave][16 * i + 4 * g + e][c] = o[q][i][e] * vtop;
+            __syncthreads();
 
-        // join the waves: 16 threads a row
-        const int r = tid >> 4, d0 = tid & 15;
-        if (row0 + r < rows) {
-            float mt = sm[0][r];
+            // join the waves: 16 threads a row
+            const int r = tid >> 4, d0 = tid & 15, mine = row0 + 16 * q + r;
+            if (mine < rows) {
+                float mt = sm[0][r];
 #pragma unroll
-            for (int w = 1; w < WAVES; ++w) mt = __builtin_fmaxf(mt, sm[w][r]);
-            const float ref = mt > -__builtin_inff() ? mt : 0.0f;
-            float f[WAVES], lt = 0.0f, lot = 0.0f;
+                for (int w = 1; w < WAVES; ++w) mt = __builtin_fmaxf(mt, sm[w][r]);
+                const float ref = mt > -__builtin_inff() ? mt : 0.0f;
+                float f[WAVES], lt = 0.0f, lot = 0.0f;
 #pragma unroll
-            for (int w = 0; w < WAVES; ++w) {
-                f[w] = __builtin_amdgcn_exp2f(sm[w][r] - ref);
-                lt += sl[w][r] * f[w];
-                lot += slo[w][r] * f[w];
+                for (int w = 0; w < WAVES; ++w) {
+                    f[w] = __builtin_amdgcn_exp2f(sm[w][r] - ref);
+                    lt += sl[w][r] * f[w];
+                    lot += slo[w][r] * f[w];
+                }
+                const int out_token = mine / a.group, out_head = head * a.group + mine % a.group;
+                const int64_t t = s.q0 + out_token, rid = t * a.q_heads + out_head;
+                const int64_t slot = piece.slot + 16 * q + r;
+                const float inv = lt == 0.0f ? 0.0f : 1.0f / lot;      // a row that sees no key: 0
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const int d = d0 + 16 * i;
+                    float v = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < WAVES; ++w) v = __builtin_fmaf(so[w][d][r], f[w], v);
+                    if (!DEAL || piece.whole) a.out[t * a.out_stride + (int64_t)out_head * D + d] = f32_to_bf16(lt == 0.0f ? 0.0f : v * inv);
+                    else a.part_o[slot * D + d] = v;
+                }
+                if (d0 == 0) {
+                    if (DEAL && !piece.whole) *reinterpret_cast<float4*>(a.part_ml + slot * 4) = make_float4(mt, lt, lot, 0.0f);
+                    else if (a.lse) a.lse[rid] = lse_of(mt, lt);
+                }
             }
-            const int out_token = (row0 + r) / a.group, out_head = head * a.group + (row0 + r) % a.group;
-            const int64_t t = s.q0 + out_token, rid = t * a.q_heads + out_head;
-            const int64_t slot = piece.slot + r;
-            const float inv = lt == 0.0f ? 0.0f : 1.0f / lot;      // a row that sees no key: 0
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const int d = d0 + 16 * i;
-                float v = 0.0f;
-#pragma unroll
-                for (int w = 0; w < WAVES; ++w) v = __builtin_fmaf(so[w][d][r], f[w], v);
-                if (!DEAL || piece.whole) a.out[t * a.out_stride + (int64_t)out_head * D + d] = f32_to_bf16(lt == 0.0f ? 0.0f : v * inv);
-                else a.part_o[slot * D + d] = v;
-            }
-            if (d0 == 0) {
-                if (DEAL && !piece.whole) *reinterpret_cast<float4*>(a.part_ml + slot * 4) = make_float4(mt, lt, lot, 0.0f);
-                else if (a.lse) a.lse[rid] = lse_of(mt, lt);
-            }
+            __syncthreads();       // before the next results
         }
-        __syncthreads();       // before the next piece's results
     } while (DEAL && next_piece(a, walks[wave], piece, x));
 }
 
@@ -676,38 +690,41 @@ __device__ __forceinline__ int64_t part_slot(const AttArgs& a, int index, int he
 // with a running maximum, then join through LDS.  A lane has 4 columns of every 64 / (D / 4)-th
 // row.  Few query rows: the pair that block blockIdx.x of the main launch began.  Many: the
 // pair's chunks.
-template <int D, bool MANY>
+template <int D, bool MANY, int R>
 __global__ __launch_bounds__(64 * WAVES) void kv8_join_kernel(AttArgs a) {
-    constexpr int LANES = D / 4, AT_ONCE = 64 / LANES, NR = ROWS / AT_ONCE;
-    __shared__ __attribute__((aligned(16))) float so[WAVES][ROWS][D];
-    __shared__ float sm[WAVES][ROWS], sl[WAVES][ROWS], slo[WAVES][ROWS];
+    constexpr int LANES = D / 4, AT_ONCE = 64 / LANES, NR = 16 / AT_ONCE;
+    __shared__ __attribute__((aligned(16))) float so[WAVES][16][D];
+    __shared__ float sm[WAVES][16], sl[WAVES][16], slo[WAVES][16];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int sub = lane / LANES, col = 4 * (lane % LANES);
     int head, count, row0, parts;
     int64_t q0, slot0, slot1;       // slots of the first part and of the second; the others follow it
-    constexpr int64_t NEXT = MANY ? P_ROWS : 2 * ROWS;
+    constexpr int64_t NEXT = MANY ? R : 2 * R;
+    const int sub0 = blockIdx.x % (R / 16) * 16;
     if constexpr (MANY) {
-        const int pair = blockIdx.x / (P_ROWS / ROWS), sub0 = blockIdx.x % (P_ROWS / ROWS) * ROWS;
+        const int pair = blockIdx.x / (R / 16);
         head = pair % a.c.heads;
-        const Item x = one_item<P_ROWS, TILE>(a, pair / a.c.heads);
+        const Item x = one_item<R, TILE>(a, pair / a.c.heads);
         parts = min(a.chunks, (x.steps + a.chunk_steps - 1) / a.chunk_steps);
         row0 = x.row0 + sub0;
-        count = min(ROWS, x.rows - row0);
+        count = min(16, x.rows - row0);
         if (parts < 2 || count <= 0) return;
         q0 = x.s.q0;
         slot0 = part_slot(a, pair / a.c.heads, head, 0) + sub0;
         slot1 = slot0 + NEXT;
     } else {
-        const int4 job = a.part_job[blockIdx.x];
+        const int block = blockIdx.x / (R / 16);
+        const int4 job = a.part_job[block];
         if (job.x < 0) return;
-        const Item x = one_item<ROWS, STEP>(a, uniform(job.x));
+        const Item x = one_item<R, STEP>(a, uniform(job.x));
         head = job.y;
-        row0 = x.row0;
-        count = min(ROWS, x.rows - row0);
+        row0 = x.row0 + sub0;
+        count = min(16, x.rows - row0);
+        if (count <= 0) return;
         q0 = x.s.q0;
-        parts = job.z - (int)blockIdx.x + 1;
-        slot0 = (2 * (int64_t)blockIdx.x + job.w) * ROWS;
-        slot1 = 2 * ((int64_t)blockIdx.x + 1) * ROWS;
+        parts = job.z - block + 1;
+        slot0 = (2 * (int64_t)block + job.w) * R + sub0;
+        slot1 = 2 * ((int64_t)block + 1) * R + sub0;
     }
 
     f32x4 v[NR];
@@ -824,7 +841,6 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
     const int wrow0 = row0 + 16 * P_QT * wave;
     const bool idle = wrow0 >= rows;
     const Span wspan = span_of(a, s, idle ? row0 : wrow0, idle ? 1 : min(16 * P_QT, rows - wrow0));
-    const bool whole = wrow0 + 16 * P_QT <= rows;
     Row row[P_QT];
     bf16x8 qf[P_QT][NS];
 #pragma unroll
@@ -964,7 +980,7 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
             }
             __builtin_amdgcn_sched_group_barrier(0x008, AHEAD * P_QT, 1);
-            const bool plain = whole && kt + TILE <= wspan.common && kt >= wspan.high && plain_tile(info);
+            const bool plain = kt + TILE <= wspan.common && kt >= wspan.high && plain_tile(info);
             if (plain) {
 #pragma unroll
                 for (int t = 0; t < P_QT; ++t) alpha[t] = softmax_plain<ONE_PAGE>(acc[t], info, want_lse, st[t], w[t]);
@@ -1007,16 +1023,11 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
     }
 }
 
-// Rows of a block: 128 where a sequence has that many, else 16 (the keys are then split over
-// the waves).
+// Rows of a block, for sequences of that many: 128, or 32 or 16 whose waves split the keys.
 template <int N>
 using Size = std::integral_constant<int, N>;
 
-bool is_prompt(int64_t max_new, int group) { return max_new * group >= PROMPT_ROWS; }
-int64_t row_tiles(int64_t max_new, int group) {
-    const int r = is_prompt(max_new, group) ? P_ROWS : ROWS;
-    return (max_new * group + r - 1) / r;
-}
+int rows_of_block(int64_t rows) { return rows >= PROMPT_ROWS ? P_ROWS : rows > 16 ? 32 : 16; }
 
 }  // namespace
 
@@ -1031,8 +1042,10 @@ int64_t row_tiles(int64_t max_new, int group) {
 AttentionPlan attention_plan(int64_t B, int64_t max_new, int64_t max_kv, int q_heads, int kv_heads, int head_dim) {
     const int group = q_heads / kv_heads;
     AttentionPlan p{};
-    p.prompt = is_prompt(max_new, group);
-    const int64_t base = B * kv_heads * row_tiles(max_new, group);
+    p.rows = rows_of_block(max_new * group);
+    p.prompt = p.rows == P_ROWS;
+    p.tiles = (max_new * group + p.rows - 1) / p.rows;
+    const int64_t base = B * kv_heads * p.tiles;
     if (p.prompt) {
         const int64_t steps = std::max<int64_t>(1, (max_kv + TILE - 1) / TILE);
         const int64_t chunk = std::max<int64_t>(6, (base * steps + 2 * DEAL_BLOCKS - 1) / (2 * DEAL_BLOCKS));
@@ -1041,15 +1054,15 @@ AttentionPlan attention_plan(int64_t B, int64_t max_new, int64_t max_kv, int q_h
         p.chunks = p.parts ? (int)((steps + chunk - 1) / chunk) : 1;
         p.chunk_steps = (int)chunk;
         p.blocks = base * p.chunks;
-        p.join_blocks = p.parts ? base * (P_ROWS / ROWS) : 0;
+        p.join_blocks = p.parts ? base * (P_ROWS / 16) : 0;
         p.part_rows = p.parts ? base * p.chunks * P_ROWS : 0;
         return p;
     }
     const int64_t steps = std::max<int64_t>(1, (max_kv + STEP - 1) / STEP);
     p.parts = steps >= 8 || steps * std::max<int64_t>(0, DEAL_BLOCKS - base) >= 3 * DEAL_BLOCKS;
-    p.blocks = p.parts ? std::min<int64_t>(DEAL_BLOCKS, base * steps) : base;
-    p.join_blocks = p.parts ? p.blocks : 0;
-    p.part_rows = p.parts ? p.blocks * 2 * ROWS : 0;
+    p.blocks = p.parts ? std::min<int64_t>(p.rows == 16 || head_dim == 64 ? DEAL_BLOCKS : DEAL_BLOCKS / 2, base * steps) : base;
+    p.join_blocks = p.parts ? p.blocks * (p.rows / 16) : 0;
+    p.part_rows = p.parts ? p.blocks * 2 * p.rows : 0;
     return p;
 }
 
@@ -1078,7 +1091,7 @@ hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const 
     a.part_job = reinterpret_cast<int4*>(a.part_ml + p.part_rows * 4);
     a.chunk_steps = p.chunk_steps;
     a.chunks = p.chunks;
-    a.tiles = (int)row_tiles(max_new, a.group);
+    a.tiles = (int)p.tiles;
     a.items = (int)(B * a.tiles);
     const dim3 grid((unsigned)p.blocks), join((unsigned)p.join_blocks);
     // pages of at least a tile: its page number and scales are one for all lanes
@@ -1092,15 +1105,18 @@ hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const 
         constexpr bool ONE = decltype(one)::value;
         if (p.prompt && p.parts) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, true>), grid, dim3(64 * P_WAVES), 0, stream, a);
         else if (p.prompt) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, false>), grid, dim3(64 * P_WAVES), 0, stream, a);
-        else if (p.parts) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, true>), grid, dim3(64 * WAVES), 0, stream, a);
-        else hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false>), grid, dim3(64 * WAVES), 0, stream, a);
+        else if (p.rows == 32 && p.parts) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, true, 2>), grid, dim3(64 * WAVES), 0, stream, a);
+        else if (p.rows == 32) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false, 2>), grid, dim3(64 * WAVES), 0, stream, a);
+        else if (p.parts) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, true, 1>), grid, dim3(64 * WAVES), 0, stream, a);
+        else hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false, 1>), grid, dim3(64 * WAVES), 0, stream, a);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.parts) return e;
     with_sizes([&](auto d, auto) {
         constexpr int D = decltype(d)::value;
-        if (p.prompt) hipLaunchKernelGGL((kv8_join_kernel<D, true>), join, dim3(64 * WAVES), 0, stream, a);
-        else hipLaunchKernelGGL((kv8_join_kernel<D, false>), join, dim3(64 * WAVES), 0, stream, a);
+        if (p.prompt) hipLaunchKernelGGL((kv8_join_kernel<D, true, P_ROWS>), join, dim3(64 * WAVES), 0, stream, a);
+        else if (p.rows == 32) hipLaunchKernelGGL((kv8_join_kernel<D, false, 32>), join, dim3(64 * WAVES), 0, stream, a);
+        else hipLaunchKernelGGL((kv8_join_kernel<D, false, 16>), join, dim3(64 * WAVES), 0, stream, a);
     });
     return hipGetLastError();
 }
