@@ -372,6 +372,7 @@ __device__ __forceinline__ int64_t wave_prefix(int64_t v, int lane) {      // in
 // Steps of all items (whole wave).
 template <int R, int S>
 __device__ __forceinline__ int64_t total_steps(const AttArgs& a, int lane) {
+    if (a.items == 1) return (int64_t)one_item<R, S>(a, 0).steps * a.c.heads;
     int64_t sum = 0;
     for (int i = 0; i < a.items; i += 64) {
         int64_t v = i + lane < a.items ? (int64_t)item_of<R, S>(a, i + lane).steps * a.c.heads : 0;
@@ -409,6 +410,8 @@ __device__ __forceinline__ Shares shares_of(int64_t total, int64_t blocks) {
 // The item that holds position `at` of the list (at < total), and where it starts.
 template <int R, int S>
 __device__ __forceinline__ int item_at(const AttArgs& a, int64_t at, int lane, int64_t& before) {
+    before = 0;
+    if (a.items == 1) return 0;
     int64_t sum = 0;
     for (int i = 0; i < a.items; i += 64) {
         const int64_t v = i + lane < a.items ? (int64_t)item_of<R, S>(a, i + lane).steps * a.c.heads : 0;
@@ -510,17 +513,18 @@ __device__ __forceinline__ bool own_item(const AttArgs& a, Piece& p, Item& x) {
 
 // A wave loads its tile straight into registers in the order of the matrix operands: the
 // values of a tile while its scores are made, the keys of the next one while its weights are
-// used.  The four waves take the step's four tiles and are joined through LDS.
-template <int D, bool ONE_PAGE, bool DEAL, int QT>
-__global__ __launch_bounds__(64 * WAVES, QT == 1 ? 2 : 1) void kv8_attention_kernel(AttArgs a) {
+// used.  The W waves take the step's W tiles and are joined through LDS.
+template <int D, bool ONE_PAGE, bool DEAL, int QT, int W>
+__global__ __launch_bounds__(64 * W, QT == 1 ? 2 : 1) void kv8_attention_kernel(AttArgs a) {
     constexpr int NK = D / 64;       // 16-byte key loads a lane and sub-tile
     constexpr int NV = D / 16;       // value column tiles
     constexpr int R = 16 * QT;       // rows of a block
+    constexpr int STEP = TILE * W;   // keys of a step
     // the waves' results, 16 rows at a time: O^T [wave][D][16 + 1], maxima and sums
-    __shared__ float so[WAVES][D][16 + 1];
-    __shared__ float sm[WAVES][16], sl[WAVES][16], slo[WAVES][16];
+    __shared__ float so[W][D][16 + 1];
+    __shared__ float sm[W][16], sl[W][16], slo[W][16];
 
-    __shared__ Walk<R, STEP> walks[WAVES];
+    __shared__ Walk<R, STEP> walks[DEAL ? W : 1];
     const int wave = uniform((int)threadIdx.x >> 6);
     Piece piece;
     Item x;
@@ -644,16 +648,16 @@ __global__ __launch_bounds__(64 * WAVES, QT == 1 ? 2 : 1) void kv8_attention_ker
                 for (int e = 0; e < 4; ++e) so[wave][16 * i + 4 * g + e][c] = o[q][i][e] * vtop;
             __syncthreads();
 
-            // join the waves: 16 threads a row
-            const int r = tid >> 4, d0 = tid & 15, mine = row0 + 16 * q + r;
+            // join the waves: 4 W threads a row
+            const int r = tid / (4 * W), d0 = tid % (4 * W), mine = row0 + 16 * q + r;
             if (mine < rows) {
                 float mt = sm[0][r];
 #pragma unroll
-                for (int w = 1; w < WAVES; ++w) mt = __builtin_fmaxf(mt, sm[w][r]);
+                for (int w = 1; w < W; ++w) mt = __builtin_fmaxf(mt, sm[w][r]);
                 const float ref = mt > -__builtin_inff() ? mt : 0.0f;
-                float f[WAVES], lt = 0.0f, lot = 0.0f;
+                float f[W], lt = 0.0f, lot = 0.0f;
 #pragma unroll
-                for (int w = 0; w < WAVES; ++w) {
+                for (int w = 0; w < W; ++w) {
                     f[w] = __builtin_amdgcn_exp2f(sm[w][r] - ref);
                     lt += sl[w][r] * f[w];
                     lot += slo[w][r] * f[w];
@@ -663,11 +667,11 @@ __global__ __launch_bounds__(64 * WAVES, QT == 1 ? 2 : 1) void kv8_attention_ker
                 const int64_t slot = piece.slot + 16 * q + r;
                 const float inv = lt == 0.0f ? 0.0f : 1.0f / lot;      // a row that sees no key: 0
 #pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const int d = d0 + 16 * i;
+                for (int i = 0; i < D / (4 * W); ++i) {
+                    const int d = d0 + 4 * W * i;
                     float v = 0.0f;
 #pragma unroll
-                    for (int w = 0; w < WAVES; ++w) v = __builtin_fmaf(so[w][d][r], f[w], v);
+                    for (int w = 0; w < W; ++w) v = __builtin_fmaf(so[w][d][r], f[w], v);
                     if (!DEAL || piece.whole) a.out[t * a.out_stride + (int64_t)out_head * D + d] = f32_to_bf16(lt == 0.0f ? 0.0f : v * inv);
                     else a.part_o[slot * D + d] = v;
                 }
@@ -1032,7 +1036,10 @@ int rows_of_block(int64_t rows) { return rows >= PROMPT_ROWS ? P_ROWS : rows > 1
 }  // namespace
 
 // Blocks of a launch.
-// Few rows (a step is 256 keys): one for each (row tile, head), or 512 (two a CU, as many as fit
+// Few rows, short contexts, few of them: a block of 8 waves for each pair, no parts (1 x 1000
+// tokens, 8 cache heads: 11.6 us against 11.9 and a launch more; 1 x 2048: 16.4 against 12.5;
+// 16 x up to 2048: 17.7 against 20.8; 16 x up to 4096: 28.1 against 27.5).
+// Few rows otherwise (a step is 256 keys): one for each (row tile, head), or 512 (two a CU, as many as fit
 // at once) that share all steps equally and whose parts are then joined.  Dealing costs a second
 // launch and pays where pairs would leave blocks idle, by three steps; lengths are uneven as a
 // rule, so contexts of eight steps are dealt however many pairs there are (16 x up to 32 k
@@ -1059,6 +1066,11 @@ AttentionPlan attention_plan(int64_t B, int64_t max_new, int64_t max_kv, int q_h
         return p;
     }
     const int64_t steps = std::max<int64_t>(1, (max_kv + STEP - 1) / STEP);
+    p.wide = p.rows == 16 && base <= 256 && max_kv <= (base < 64 ? 1024 : 2048);
+    if (p.wide) {
+        p.blocks = base;
+        return p;
+    }
     p.parts = steps >= 8 || steps * std::max<int64_t>(0, DEAL_BLOCKS - base) >= 3 * DEAL_BLOCKS;
     p.blocks = p.parts ? std::min<int64_t>(p.rows == 16 || head_dim == 64 ? DEAL_BLOCKS : DEAL_BLOCKS / 2, base * steps) : base;
     p.join_blocks = p.parts ? p.blocks * (p.rows / 16) : 0;
@@ -1105,10 +1117,11 @@ hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const 
         constexpr bool ONE = decltype(one)::value;
         if (p.prompt && p.parts) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, true>), grid, dim3(64 * P_WAVES), 0, stream, a);
         else if (p.prompt) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, false>), grid, dim3(64 * P_WAVES), 0, stream, a);
-        else if (p.rows == 32 && p.parts) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, true, 2>), grid, dim3(64 * WAVES), 0, stream, a);
-        else if (p.rows == 32) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false, 2>), grid, dim3(64 * WAVES), 0, stream, a);
-        else if (p.parts) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, true, 1>), grid, dim3(64 * WAVES), 0, stream, a);
-        else hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false, 1>), grid, dim3(64 * WAVES), 0, stream, a);
+        else if (p.wide) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false, 1, 2 * WAVES>), grid, dim3(128 * WAVES), 0, stream, a);
+        else if (p.rows == 32 && p.parts) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, true, 2, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
+        else if (p.rows == 32) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false, 2, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
+        else if (p.parts) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, true, 1, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
+        else hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false, 1, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.parts) return e;
