@@ -690,15 +690,16 @@ __device__ __forceinline__ int64_t part_slot(const AttArgs& a, int index, int he
     return (((int64_t)index * a.c.heads + head) * a.chunks + chunk) * P_ROWS;
 }
 
-// Joins the parts of one (row tile, head) pair, 16 rows a block: the waves take parts in turn
-// with a running maximum, then join through LDS.  A lane has 4 columns of every 64 / (D / 4)-th
-// row.  Few query rows: the pair that block blockIdx.x of the main launch began.  Many: the
+// Joins the parts of one (row tile, head) pair, 16 rows a block: the W waves take parts in turn,
+// four at a time (their loads are what this kernel waits for), with a running maximum, then
+// join through LDS; of many query rows, with few parts each, they take rows in turn instead.  A lane has 4 columns of every 64 / (D / 4)-th row.  Few query rows: the pair that block blockIdx.x of the main launch began.  Many: the
 // pair's chunks.
-template <int D, bool MANY, int R>
-__global__ __launch_bounds__(64 * WAVES) void kv8_join_kernel(AttArgs a) {
+template <int D, bool MANY, int R, int W>
+__global__ __launch_bounds__(64 * W) void kv8_join_kernel(AttArgs a) {
     constexpr int LANES = D / 4, AT_ONCE = 64 / LANES, NR = 16 / AT_ONCE;
-    __shared__ __attribute__((aligned(16))) float so[WAVES][16][D];
-    __shared__ float sm[WAVES][16], sl[WAVES][16], slo[WAVES][16];
+    constexpr int SHARE = MANY ? 1 : W;      // waves that share a row's parts
+    __shared__ __attribute__((aligned(16))) float so[SHARE][16][D];
+    __shared__ float sm[SHARE][16], sl[SHARE][16], slo[SHARE][16];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int sub = lane / LANES, col = 4 * (lane % LANES);
     int head, count, row0, parts;
@@ -731,49 +732,71 @@ __global__ __launch_bounds__(64 * WAVES) void kv8_join_kernel(AttArgs a) {
         slot1 = 2 * ((int64_t)block + 1) * R + sub0;
     }
 
-    f32x4 v[NR];
-    float m[NR], l[NR], lo[NR];
+    auto finish = [&](int r, int d, f32x4 y, float mt, float lt, float lot) {
+        const int64_t t = q0 + (row0 + r) / a.group;
+        const int qh = head * a.group + (row0 + r) % a.group;
+        const float inv = 1.0f / lot;
+        *reinterpret_cast<uint2*>(a.out + t * a.out_stride + (int64_t)qh * D + d) =
+            lt == 0.0f ? make_uint2(0, 0) : make_uint2(f32x2_to_bf16x2(y[0] * inv, y[1] * inv), f32x2_to_bf16x2(y[2] * inv, y[3] * inv));
+        if (a.lse && d == 0) a.lse[t * a.q_heads + qh] = lse_of(mt, lt);
+    };
+#pragma unroll 1
+    for (int j = MANY ? wave : 0; j < NR; j += MANY ? W : 1) {
+        const int r = AT_ONCE * j + sub;
+        if (AT_ONCE * j >= count) break;
+        const int rr = r < count ? r : count - 1;
+        f32x4 v = {0, 0, 0, 0};
+        float m = -__builtin_inff(), l = 0.0f, lo = 0.0f;
+        for (int i = MANY ? 0 : wave; i < parts; i += 4 * SHARE) {
+            float4 ml[4];
+            f32x4 p[4];
 #pragma unroll
-    for (int j = 0; j < NR; ++j) {
-        v[j] = f32x4{0, 0, 0, 0};
-        m[j] = -__builtin_inff();
-        l[j] = lo[j] = 0.0f;
-    }
-    for (int i = wave; i < parts; i += WAVES) {
-        const int64_t slot = i == 0 ? slot0 : slot1 + (i - 1) * NEXT;
+            for (int u = 0; u < 4; ++u) {
+                const int part = i + u * SHARE < parts ? i + u * SHARE : i;
+                const int64_t slot = (part == 0 ? slot0 : slot1 + (part - 1) * NEXT) + rr;
+                ml[u] = *reinterpret_cast<const float4*>(a.part_ml + slot * 4);
+                p[u] = *reinterpret_cast<const f32x4*>(a.part_o + slot * D + col);
+            }
+            float mn = m;
 #pragma unroll
-        for (int j = 0; j < NR; ++j) {
-            const int r = AT_ONCE * j + sub;
-            if (r >= count) continue;
-            const float4 ml = *reinterpret_cast<const float4*>(a.part_ml + (slot + r) * 4);
-            const f32x4 p = *reinterpret_cast<const f32x4*>(a.part_o + (slot + r) * D + col);
-            const float mn = __builtin_fmaxf(m[j], ml.x), ref = mn > -__builtin_inff() ? mn : 0.0f;
-            const float f0 = __builtin_amdgcn_exp2f(m[j] - ref), f1 = __builtin_amdgcn_exp2f(ml.x - ref);
-            m[j] = mn;
-            l[j] = l[j] * f0 + ml.y * f1;
-            lo[j] = lo[j] * f0 + ml.z * f1;
+            for (int u = 0; u < 4; ++u) {
+                if (i + u * SHARE >= parts) ml[u].x = -__builtin_inff();       // counted already
+                mn = __builtin_fmaxf(mn, ml[u].x);
+            }
+            const float ref = mn > -__builtin_inff() ? mn : 0.0f, old = __builtin_amdgcn_exp2f(m - ref);
+            m = mn;
+            l *= old;
+            lo *= old;
+            v *= old;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[j][e] = __builtin_fmaf(p[e], f1, v[j][e] * f0);
+            for (int u = 0; u < 4; ++u) {
+                const float f = __builtin_amdgcn_exp2f(ml[u].x - ref);
+                l = __builtin_fmaf(ml[u].y, f, l);
+                lo = __builtin_fmaf(ml[u].z, f, lo);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(p[u][e], f, v[e]);
+            }
+        }
+        if (r >= count) continue;
+        if constexpr (MANY) {
+            finish(r, col, v, m, l, lo);
+        } else {
+            *reinterpret_cast<f32x4*>(&so[wave][r][col]) = v;
+            if (col == 0) { sm[wave][r] = m; sl[wave][r] = l; slo[wave][r] = lo; }
         }
     }
-#pragma unroll
-    for (int j = 0; j < NR; ++j) {
-        const int r = AT_ONCE * j + sub;
-        if (r >= count) continue;
-        *reinterpret_cast<f32x4*>(&so[wave][r][col]) = v[j];
-        if (col == 0) { sm[wave][r] = m[j]; sl[wave][r] = l[j]; slo[wave][r] = lo[j]; }
-    }
+    if constexpr (MANY) return;
     __syncthreads();
-    for (int i = tid; i < count * LANES; i += 64 * WAVES) {
+    for (int i = tid; i < count * LANES; i += 64 * W) {
         const int r = i / LANES, d = 4 * (i % LANES);
         float mt = sm[0][r];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) mt = __builtin_fmaxf(mt, sm[w][r]);
+        for (int w = 1; w < SHARE; ++w) mt = __builtin_fmaxf(mt, sm[w][r]);
         const float ref = mt > -__builtin_inff() ? mt : 0.0f;
         float lt = 0.0f, lot = 0.0f;
         f32x4 y = {0, 0, 0, 0};
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
+        for (int w = 0; w < SHARE; ++w) {
             const float f = __builtin_amdgcn_exp2f(sm[w][r] - ref);
             lt += sl[w][r] * f;
             lot += slo[w][r] * f;
@@ -781,12 +804,7 @@ __global__ __launch_bounds__(64 * WAVES) void kv8_join_kernel(AttArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(p[e], f, y[e]);
         }
-        const int64_t t = q0 + (row0 + r) / a.group;
-        const int qh = head * a.group + (row0 + r) % a.group;
-        const float inv = 1.0f / lot;
-        *reinterpret_cast<uint2*>(a.out + t * a.out_stride + (int64_t)qh * D + d) =
-            lt == 0.0f ? make_uint2(0, 0) : make_uint2(f32x2_to_bf16x2(y[0] * inv, y[1] * inv), f32x2_to_bf16x2(y[2] * inv, y[3] * inv));
-        if (a.lse && d == 0) a.lse[t * a.q_heads + qh] = lse_of(mt, lt);
+        finish(r, d, y, mt, lt, lot);
     }
 }
 
@@ -1127,9 +1145,9 @@ hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const 
     if (e != hipSuccess || !p.parts) return e;
     with_sizes([&](auto d, auto) {
         constexpr int D = decltype(d)::value;
-        if (p.prompt) hipLaunchKernelGGL((kv8_join_kernel<D, true, P_ROWS>), join, dim3(64 * WAVES), 0, stream, a);
-        else if (p.rows == 32) hipLaunchKernelGGL((kv8_join_kernel<D, false, 32>), join, dim3(64 * WAVES), 0, stream, a);
-        else hipLaunchKernelGGL((kv8_join_kernel<D, false, 16>), join, dim3(64 * WAVES), 0, stream, a);
+        if (p.prompt) hipLaunchKernelGGL((kv8_join_kernel<D, true, P_ROWS, 4>), join, dim3(256), 0, stream, a);
+        else if (p.rows == 32) hipLaunchKernelGGL((kv8_join_kernel<D, false, 32, 8>), join, dim3(512), 0, stream, a);
+        else hipLaunchKernelGGL((kv8_join_kernel<D, false, 16, 8>), join, dim3(512), 0, stream, a);
     });
     return hipGetLastError();
 }
