@@ -514,13 +514,13 @@ __device__ __forceinline__ bool own_item(const AttArgs& a, Piece& p, Item& x) {
 // A wave loads its tile straight into registers in the order of the matrix operands: the
 // values of a tile while its scores are made, the keys of the next one while its weights are
 // used.  The W waves take the step's W tiles and are joined through LDS.
-template <int D, bool ONE_PAGE, bool DEAL, int QT, int W>
-__global__ __launch_bounds__(64 * W, QT == 1 ? 2 : 1) void kv8_attention_kernel(AttArgs a) {
+template <int D, bool ONE_PAGE, bool DEAL, int W>
+__global__ __launch_bounds__(64 * W, 2) void kv8_attention_kernel(AttArgs a) {
     constexpr int NK = D / 64;       // 16-byte key loads a lane and sub-tile
     constexpr int NV = D / 16;       // value column tiles
-    constexpr int R = 16 * QT;       // rows of a block
+    constexpr int R = 16;            // rows of a block
     constexpr int STEP = TILE * W;   // keys of a step
-    // the waves' results, 16 rows at a time: O^T [wave][D][16 + 1], maxima and sums
+    // the waves' results: O^T [wave][D][16 + 1], maxima and sums
     __shared__ float so[W][D][16 + 1];
     __shared__ float sm[W][16], sl[W][16], slo[W][16];
 
@@ -549,21 +549,18 @@ __global__ __launch_bounds__(64 * W, QT == 1 ? 2 : 1) void kv8_attention_kernel(
         const int first = (span.low / STEP + piece.step) * STEP;
         const int k0 = first + wave * TILE, k1 = min(span.top, first + piece.steps * STEP);
 
-        Row row[QT];
-        bf16x8 qf[QT][2 * NK];
-        RowState st[QT];
-        f32x4 o[QT][NV];
-#pragma unroll
-        for (int q = 0; q < QT; ++q) {
-            row[q] = row_of(a, s, head, row0 + 16 * q + c, rows);
-            const uint16_t* src = a.q + (s.q0 + row[q].token) * a.q_stride + (int64_t)row[q].head * D + 16 * g;
+        const Row row = row_of(a, s, head, row0 + c, rows);
+        bf16x8 qf[2 * NK];
+        {
+            const uint16_t* src = a.q + (s.q0 + row.token) * a.q_stride + (int64_t)row.head * D + 16 * g;
 #pragma unroll
             for (int i = 0; i < 2 * NK; ++i)
-                qf[q][i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(src + 64 * (i >> 1) + 8 * (i & 1)));
-            st[q] = fresh_row();
-#pragma unroll
-            for (int i = 0; i < NV; ++i) o[q][i] = f32x4{0, 0, 0, 0};
+                qf[i] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(src + 64 * (i >> 1) + 8 * (i & 1)));
         }
+        RowState st = fresh_row();
+        f32x4 o[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) o[i] = f32x4{0, 0, 0, 0};
 
         // lane (c, g): keys from row c of a sub-tile (tokens 16 (c / 4) + 4 j + c % 4), 16 codes
         // of every 64; values of tokens 16 g .. 16 g + 15.  Page numbers are fetched a step
@@ -601,87 +598,74 @@ __global__ __launch_bounds__(64 * W, QT == 1 ? 2 : 1) void kv8_attention_kernel(
             const bool more = kt + STEP < k1;
             if (more) pages(kt + STEP);
 
-            f32x4 acc[QT][4];
+            f32x4 acc[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                for (int q = 0; q < QT; ++q) acc[q][j] = f32x4{0, 0, 0, 0};
+                acc[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int i = 0; i < NK; ++i) {
                     const uint4 w = kw[j * NK + i];
-                    const bf16x8 lo = widen(w.x, w.y), hi = widen(w.z, w.w);
-#pragma unroll
-                    for (int q = 0; q < QT; ++q) acc[q][j] = mfma(lo, qf[q][2 * i], acc[q][j]);
-#pragma unroll
-                    for (int q = 0; q < QT; ++q) acc[q][j] = mfma(hi, qf[q][2 * i + 1], acc[q][j]);
+                    acc[j] = mfma(widen(w.x, w.y), qf[2 * i], acc[j]);
+                    acc[j] = mfma(widen(w.z, w.w), qf[2 * i + 1], acc[j]);
                 }
             }
             if (more) load_keys(kt + STEP);
             const TileInfo t = tile_info<ONE_PAGE>(ks, vs, a.scale_log2, kt + 16 * g, present);
             const bool plain = kt + TILE <= span.common && kt >= span.high && plain_tile(t);
-            Weights w[QT];
+            Weights w;
+            const float alpha = plain ? softmax_plain<ONE_PAGE>(acc, t, want_lse, st, w)
+                                      : softmax_any(acc, t, row.begin, row.end, st, w);
+            if (__any(alpha != 1.0f)) {
 #pragma unroll
-            for (int q = 0; q < QT; ++q) {
-                const float alpha = plain ? softmax_plain<ONE_PAGE>(acc[q], t, want_lse, st[q], w[q])
-                                          : softmax_any(acc[q], t, row[q].begin, row[q].end, st[q], w[q]);
-                if (__any(alpha != 1.0f)) {
-#pragma unroll
-                    for (int i = 0; i < NV; ++i) o[q][i] *= alpha;
-                }
+                for (int i = 0; i < NV; ++i) o[i] *= alpha;
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const f16x8 lo = widen_f16(vw[i].x, vw[i].y), hi = widen_f16(vw[i].z, vw[i].w);
-#pragma unroll
-                for (int q = 0; q < QT; ++q) o[q][i] = mfma(lo, w[q].lo, o[q][i]);
-#pragma unroll
-                for (int q = 0; q < QT; ++q) o[q][i] = mfma(hi, w[q].hi, o[q][i]);
+                o[i] = mfma(widen_f16(vw[i].x, vw[i].y), w.lo, o[i]);
+                o[i] = mfma(widen_f16(vw[i].z, vw[i].w), w.hi, o[i]);
             }
         }
+        const float vtop = __builtin_amdgcn_exp2f(st.lv);
+        if (g == 0) { sm[wave][c] = st.m; sl[wave][c] = st.l; slo[wave][c] = st.lo; }
 #pragma unroll
-        for (int q = 0; q < QT; ++q) {
-            const float vtop = __builtin_amdgcn_exp2f(st[q].lv);
-            if (g == 0) { sm[wave][c] = st[q].m; sl[wave][c] = st[q].l; slo[wave][c] = st[q].lo; }
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) so[wave][16 * i + 4 * g + e][c] = o[q][i][e] * vtop;
-            __syncthreads();
+            for (int e = 0; e < 4; ++e) so[wave][16 * i + 4 * g + e][c] = o[i][e] * vtop;
+        __syncthreads();
 
-            // join the waves: 4 W threads a row
-            const int r = tid / (4 * W), d0 = tid % (4 * W), mine = row0 + 16 * q + r;
-            if (mine < rows) {
-                float mt = sm[0][r];
+        // join the waves: 4 W threads a row
+        const int r = tid / (4 * W), d0 = tid % (4 * W), mine = row0 + r;
+        if (mine < rows) {
+            float mt = sm[0][r];
 #pragma unroll
-                for (int w = 1; w < W; ++w) mt = __builtin_fmaxf(mt, sm[w][r]);
-                const float ref = mt > -__builtin_inff() ? mt : 0.0f;
-                float f[W], lt = 0.0f, lot = 0.0f;
+            for (int w = 1; w < W; ++w) mt = __builtin_fmaxf(mt, sm[w][r]);
+            const float ref = mt > -__builtin_inff() ? mt : 0.0f;
+            float f[W], lt = 0.0f, lot = 0.0f;
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    f[w] = __builtin_amdgcn_exp2f(sm[w][r] - ref);
-                    lt += sl[w][r] * f[w];
-                    lot += slo[w][r] * f[w];
-                }
-                const int out_token = mine / a.group, out_head = head * a.group + mine % a.group;
-                const int64_t t = s.q0 + out_token, rid = t * a.q_heads + out_head;
-                const int64_t slot = piece.slot + 16 * q + r;
-                const float inv = lt == 0.0f ? 0.0f : 1.0f / lot;      // a row that sees no key: 0
-#pragma unroll
-                for (int i = 0; i < D / (4 * W); ++i) {
-                    const int d = d0 + 4 * W * i;
-                    float v = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < W; ++w) v = __builtin_fmaf(so[w][d][r], f[w], v);
-                    if (!DEAL || piece.whole) a.out[t * a.out_stride + (int64_t)out_head * D + d] = f32_to_bf16(lt == 0.0f ? 0.0f : v * inv);
-                    else a.part_o[slot * D + d] = v;
-                }
-                if (d0 == 0) {
-                    if (DEAL && !piece.whole) *reinterpret_cast<float4*>(a.part_ml + slot * 4) = make_float4(mt, lt, lot, 0.0f);
-                    else if (a.lse) a.lse[rid] = lse_of(mt, lt);
-                }
+            for (int w = 0; w < W; ++w) {
+                f[w] = __builtin_amdgcn_exp2f(sm[w][r] - ref);
+                lt += sl[w][r] * f[w];
+                lot += slo[w][r] * f[w];
             }
-            __syncthreads();       // before the next results
+            const int out_token = mine / a.group, out_head = head * a.group + mine % a.group;
+            const int64_t t = s.q0 + out_token, rid = t * a.q_heads + out_head;
+            const int64_t slot = piece.slot + r;
+            const float inv = lt == 0.0f ? 0.0f : 1.0f / lot;      // a row that sees no key: 0
+#pragma unroll
+            for (int i = 0; i < D / (4 * W); ++i) {
+                const int d = d0 + 4 * W * i;
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) v = __builtin_fmaf(so[w][d][r], f[w], v);
+                if (!DEAL || piece.whole) a.out[t * a.out_stride + (int64_t)out_head * D + d] = f32_to_bf16(lt == 0.0f ? 0.0f : v * inv);
+                else a.part_o[slot * D + d] = v;
+            }
+            if (d0 == 0) {
+                if (DEAL && !piece.whole) *reinterpret_cast<float4*>(a.part_ml + slot * 4) = make_float4(mt, lt, lot, 0.0f);
+                else if (a.lse) a.lse[rid] = lse_of(mt, lt);
+            }
         }
+        __syncthreads();       // before the next results
     } while (DEAL && next_piece(a, walks[wave], piece, x));
 }
 
@@ -1045,11 +1029,13 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
     }
 }
 
-// Rows of a block, for sequences of that many: 128, or 32 or 16 whose waves split the keys.
+// Rows of a block, for sequences of that many: 128, or 16 whose waves split the keys (further row
+// tiles find the keys in the L2 cache: blocks of 32 rows were 5 to 10 % slower on 5 to 16 tokens
+// a sequence).
 template <int N>
 using Size = std::integral_constant<int, N>;
 
-int rows_of_block(int64_t rows) { return rows >= PROMPT_ROWS ? P_ROWS : rows > 16 ? 32 : 16; }
+int rows_of_block(int64_t rows) { return rows >= PROMPT_ROWS ? P_ROWS : 16; }
 
 }  // namespace
 
@@ -1090,7 +1076,7 @@ AttentionPlan attention_plan(int64_t B, int64_t max_new, int64_t max_kv, int q_h
         return p;
     }
     p.parts = steps >= 8 || steps * std::max<int64_t>(0, DEAL_BLOCKS - base) >= 3 * DEAL_BLOCKS;
-    p.blocks = p.parts ? std::min<int64_t>(p.rows == 16 || head_dim == 64 ? DEAL_BLOCKS : DEAL_BLOCKS / 2, base * steps) : base;
+    p.blocks = p.parts ? std::min<int64_t>(DEAL_BLOCKS, base * steps) : base;
     p.join_blocks = p.parts ? p.blocks * (p.rows / 16) : 0;
     p.part_rows = p.parts ? p.blocks * 2 * p.rows : 0;
     return p;
@@ -1135,18 +1121,15 @@ hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const 
         constexpr bool ONE = decltype(one)::value;
         if (p.prompt && p.parts) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, true>), grid, dim3(64 * P_WAVES), 0, stream, a);
         else if (p.prompt) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, false>), grid, dim3(64 * P_WAVES), 0, stream, a);
-        else if (p.wide) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false, 1, 2 * WAVES>), grid, dim3(128 * WAVES), 0, stream, a);
-        else if (p.rows == 32 && p.parts) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, true, 2, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
-        else if (p.rows == 32) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false, 2, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
-        else if (p.parts) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, true, 1, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
-        else hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false, 1, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
+        else if (p.wide) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false, 2 * WAVES>), grid, dim3(128 * WAVES), 0, stream, a);
+        else if (p.parts) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, true, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
+        else hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.parts) return e;
     with_sizes([&](auto d, auto) {
         constexpr int D = decltype(d)::value;
         if (p.prompt) hipLaunchKernelGGL((kv8_join_kernel<D, true, P_ROWS, 4>), join, dim3(256), 0, stream, a);
-        else if (p.rows == 32) hipLaunchKernelGGL((kv8_join_kernel<D, false, 32, 8>), join, dim3(512), 0, stream, a);
         else hipLaunchKernelGGL((kv8_join_kernel<D, false, 16, 8>), join, dim3(512), 0, stream, a);
     });
     return hipGetLastError();
