@@ -25,7 +25,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import w4a8
-from .w4a8 import ROT_BLOCK, _check, _dev, _out
+from .w4a8 import ROT_BLOCK, _check, _dev
 
 ABI_VERSION = 1
 NORM_MAX_K, ROPE_MAX_AXES, ROPE_MAX_HEAD_DIM = 16384, 4, 256
@@ -81,9 +81,24 @@ def call(fn: str, *args) -> int:
     return getattr(load(), fn)(*args)
 
 
+def _new_or(t, shape, dtype, device, name: str) -> torch.Tensor:
+    """A caller's output buffer, checked, or a new one."""
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else _is(t, shape, dtype, name)
+
+
 def _stream(t: torch.Tensor) -> int:
     """The current stream's handle; without building a torch Stream object, which costs as much as half a launch."""
     return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _is(t, shape, dtype, name: str) -> torch.Tensor:
+    """A given tensor must be on the GPU, dense, and exactly of this shape and type."""
+    if t.__class__ is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t
+    _dev(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -113,32 +128,21 @@ def _heads(x: torch.Tensor, name: str, heads: Optional[int] = None, head_dim: Op
     return stride[0] if t > 1 else h * d
 
 
-def _ints(x: torch.Tensor, name: str, n: int) -> torch.Tensor:
-    _dev(x, torch.int32, name)
-    if tuple(x.shape) != (n,):
-        raise ValueError(f"{name} must have shape ({n},), got {tuple(x.shape)}")
-    return x
-
-
-def _weight(weight: torch.Tensor, k: int) -> None:
-    _dev(weight, torch.float32, "weight")
-    if tuple(weight.shape) != (k,):
-        raise ValueError(f"weight must have shape ({k},), got {tuple(weight.shape)}")
 
 
 def _norm(m, k, x, weight, residual, eps, qmax, h, rstd, y, xq, xs):
-    _weight(weight, k)
+    _is(weight, (k,), torch.float32, "weight")
     stream = torch.bfloat16
     if residual is not None:
         stream = residual.dtype
         if stream not in _STREAM_TYPES:
             raise ValueError("residual must be bfloat16 or float32")
-        _out(residual, (m, k), stream, x.device, "residual")
-        h = _out(h, (m, k), stream, x.device, "h")
+        _is(residual, (m, k), stream, "residual")
+        h = _new_or(h, (m, k), stream, x.device, "h")
     elif h is not None:
         raise ValueError("h is an output only where there is a residual")
     if rstd is not None:
-        _out(rstd, (m,), torch.float32, x.device, "rstd")
+        _is(rstd, (m,), torch.float32, "rstd")
     _check("rmsnorm_quant_act", load().rmsnorm_quant_act(
         x.data_ptr(), _ptr(residual), _STREAM_TYPES[stream], weight.data_ptr(), m, k, eps, ROT_BLOCK, qmax, _ptr(h),
         _ptr(rstd), _ptr(y), _ptr(xq), _ptr(xs), _stream(x)))
@@ -153,17 +157,17 @@ def rmsnorm_quant_act(x, weight, residual=None, eps: float = 1e-6, qmax: int = 1
     ``h`` may be the residual itself (updated in place).  ``rstd`` float32 [M] and ``y``
     bf16 [M, K] (the normalised rows, unrotated) are written if given."""
     m, k = _rows(x, "x")
-    xq = _out(xq, (m, k), torch.int8, x.device, "xq")
-    xs = _out(xs, (m,), torch.float32, x.device, "xs")
+    xq = _new_or(xq, (m, k), torch.int8, x.device, "xq")
+    xs = _new_or(xs, (m,), torch.float32, x.device, "xs")
     if y is not None:
-        _out(y, (m, k), torch.bfloat16, x.device, "y")
+        _is(y, (m, k), torch.bfloat16, "y")
     return xq, xs, _norm(m, k, x, weight, residual, eps, qmax, h, rstd, y, xq, xs)
 
 
 def rmsnorm(x, weight, residual=None, eps: float = 1e-6, h=None, rstd=None, y=None):
     """The same norm without the int8 rows (a final norm): (y bf16 [M, K], h)."""
     m, k = _rows(x, "x")
-    y = _out(y, (m, k), torch.bfloat16, x.device, "y")
+    y = _new_or(y, (m, k), torch.bfloat16, x.device, "y")
     return y, _norm(m, k, x, weight, residual, eps, 127, h, rstd, y, None, None)
 
 
@@ -176,18 +180,18 @@ def rmsnorm_grad(grad, h, rstd, weight, grad_h=None, rotated: bool = True, dx=No
     without need_dweight.  ``workspace``: a uint8 tensor of rmsnorm_grad_workspace(M, K)
     bytes at least, allocated if None."""
     m, k = _rows(grad, "grad")
-    _weight(weight, k)
+    _is(weight, (k,), torch.float32, "weight")
     dt = h.dtype
     if dt not in _STREAM_TYPES:
         raise ValueError("h must be bfloat16 or float32")
-    _out(h, (m, k), dt, grad.device, "h")
-    _out(rstd, (m,), torch.float32, grad.device, "rstd")
+    _is(h, (m, k), dt, "h")
+    _is(rstd, (m,), torch.float32, "rstd")
     if grad_h is not None:
-        _out(grad_h, (m, k), dt, grad.device, "grad_h")
-    dx = _out(dx, (m, k), dt, grad.device, "dx")
+        _is(grad_h, (m, k), dt, "grad_h")
+    dx = _new_or(dx, (m, k), dt, grad.device, "dx")
     lib, ws = load(), 0
     if need_dweight:
-        dweight = _out(dweight, (k,), torch.float32, grad.device, "dweight")
+        dweight = _new_or(dweight, (k,), torch.float32, grad.device, "dweight")
         ws = lib.rmsnorm_grad_workspace(m, k)
         workspace = _workspace(workspace, ws, grad.device)
     elif dweight is not None:
@@ -228,9 +232,7 @@ class Rope:
         sections = [n] if self.sections is None else list(self.sections)
         if not 1 <= len(sections) <= ROPE_MAX_AXES:
             raise ValueError(f"1 to {ROPE_MAX_AXES} axes, got {len(sections)}")
-        _dev(pos, torch.int32, "pos")
-        if tuple(pos.shape) != (len(sections), tokens):
-            raise ValueError(f"pos must have shape ({len(sections)}, {tokens}), got {tuple(pos.shape)}")
+        _is(pos, (len(sections), tokens), torch.int32, "pos")
         return RopeDesc(pos.data_ptr(), tokens, self.inv_freq.data_ptr(), 2 * n, len(sections),
                         (_I32 * ROPE_MAX_AXES)(*sections), int(bool(self.interleaved)))
 
@@ -272,9 +274,9 @@ class KVCache8:
         if self.k.dim() != 4:
             raise ValueError("cache.k must be [pages, heads, page_tokens, head_dim]")
         pages, heads, tokens, d = self.k.shape
-        _out(self.v, (pages, heads, d, tokens), torch.int8, self.k.device, "cache.v")
-        _out(self.k_scale, (pages, heads), torch.float32, self.k.device, "cache.k_scale")
-        _out(self.v_scale, (pages, heads), torch.float32, self.k.device, "cache.v_scale")
+        _is(self.v, (pages, heads, d, tokens), torch.int8, "cache.v")
+        _is(self.k_scale, (pages, heads), torch.float32, "cache.k_scale")
+        _is(self.v_scale, (pages, heads), torch.float32, "cache.v_scale")
         _dev(table, torch.int32, "table")
         if table.dim() != 2 or table.shape[0] != batch:
             raise ValueError(f"table must be [{batch}, pages of a sequence], got {tuple(table.shape)}")
@@ -291,8 +293,8 @@ def kv8_append(cache: KVCache8, table, ctx_len, q_start, max_new: int, k, v, q=N
     With ``q`` bf16 [T, q_heads, head_dim] its rotation is returned (into ``q_out``)."""
     batch = ctx_len.numel()
     desc = cache.desc(table, batch)
-    _ints(ctx_len, "ctx_len", batch)
-    _ints(q_start, "q_start", batch + 1)
+    _is(ctx_len, (batch,), torch.int32, "ctx_len")
+    _is(q_start, (batch + 1,), torch.int32, "q_start")
     heads, d = cache.k.shape[1], cache.k.shape[3]
     ks = _heads(k, "k", heads, d)
     t = k.shape[0]
@@ -325,8 +327,8 @@ def kv8_attention(q, cache: KVCache8, table, kv_len, q_start, max_new: int, max_
     kv8_attention_workspace(...) bytes at least, allocated if None."""
     batch = kv_len.numel()
     desc = cache.desc(table, batch)
-    _ints(kv_len, "kv_len", batch)
-    _ints(q_start, "q_start", batch + 1)
+    _is(kv_len, (batch,), torch.int32, "kv_len")
+    _is(q_start, (batch + 1,), torch.int32, "q_start")
     heads, d = cache.k.shape[1], cache.k.shape[3]
     qs = _heads(q, "q", None, d)
     t, qh, _ = q.shape
@@ -334,7 +336,7 @@ def kv8_attention(q, cache: KVCache8, table, kv_len, q_start, max_new: int, max_
         out = torch.empty(t, qh, d, dtype=torch.bfloat16, device=q.device)
     os_ = _heads(out, "out", qh, d, t)
     if lse is not None:
-        _out(lse, (t, qh), torch.float32, q.device, "lse")
+        _is(lse, (t, qh), torch.float32, "lse")
     lib = load()
     ws = lib.kv8_attention_workspace(batch, t, max_new, max_kv, qh, heads, d)
     workspace = _workspace(workspace, ws, q.device)

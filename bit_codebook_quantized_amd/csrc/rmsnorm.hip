@@ -153,8 +153,23 @@ __global__ __launch_bounds__(1024) void rmsnorm_grad_kernel(const uint16_t* __re
         }
         if (ok) store16(dx + at, g);
     }
-    if (partial) store16(partial + ((int64_t)blockIdx.x * rows + pl.row_local) * K + col, dw);
+    if (!partial) return;
+    if (rows > 1) {      // one partial row a block: its rows' sums are added in their order
+        float* const all = lds + 128;
+        __syncthreads();
+        store16(all + pl.row_local * K + col, dw);
+        __syncthreads();
+        if (pl.row_local > 0) return;
+        for (int r = 1; r < rows; ++r) {
+            float other[16];
+            load16(all + r * K + col, other);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dw[i] += other[i];
+        }
+    }
+    store16(partial + (int64_t)blockIdx.x * K + col, dw);
 }
+static_assert(16 * 256 <= 16 * NT_SLOT, "the columns of 16 slots fit in their tiles");
 
 // dweight[k] = sum over the partial rows: 64 columns a block, 4 a lane (256-byte row pieces), 64
 // lanes down the rows, then their sums through LDS, each in a fixed order.
@@ -227,7 +242,7 @@ hipError_t launch_rmsnorm_quant(const void* x, const void* residual, int stream_
     return launch_norm<uint16_t, true>(x, residual, weight, M, K, eps, qmax, h, rstd, y, xq, xs, stream);
 }
 
-int64_t rmsnorm_grad_partial_rows(int64_t M, int K) { return grad_blocks(M, K >> 8) * norm_rows(K >> 8); }
+int64_t rmsnorm_grad_partial_rows(int64_t M, int K) { return grad_blocks(M, K >> 8); }
 
 hipError_t launch_rmsnorm_grad(const void* grad, const void* h, int stream_f32, const float* rstd, const float* weight,
                                const void* grad_h, int64_t M, int K, int rot, void* dx, float* dweight,
