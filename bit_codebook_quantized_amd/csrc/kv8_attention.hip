@@ -317,8 +317,9 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l) - W_EXP) * 0.69314718055994531f;
 }
 
-// Many query rows: from this many rows of a sequence on; waves, 16-row tiles a wave, rows of a block.
-constexpr int PROMPT_ROWS = 128, P_WAVES = 4, P_QT = 2, P_ROWS = 16 * P_QT * P_WAVES;
+// Many query rows: from this many rows of a sequence on; waves of a block, each with one or two
+// tiles of 16 rows.
+constexpr int PROMPT_ROWS = 64, P_WAVES = 4;
 
 // How the work of few query rows is dealt.  It is a list of steps: for every sequence, row tile (R rows) and
 // head, the steps of S keys that its rows see.  The list is dealt to the blocks in equal
@@ -673,9 +674,10 @@ __global__ __launch_bounds__(64 * W, 2) void kv8_attention_kernel(AttArgs a) {
     } while (DEAL && next_piece(a, walks[wave], piece, x));
 }
 
-// First part row of a (row tile, head) pair's chunk (many query rows).
+// First part row of a (row tile, head) pair's chunk (many query rows, R a block).
+template <int R>
 __device__ __forceinline__ int64_t part_slot(const AttArgs& a, int index, int head, int chunk) {
-    return (((int64_t)index * a.c.heads + head) * a.chunks + chunk) * P_ROWS;
+    return (((int64_t)index * a.c.heads + head) * a.chunks + chunk) * R;
 }
 
 // Joins the parts of one (row tile, head) pair, 16 rows a block: the W waves take parts in turn,
@@ -703,7 +705,7 @@ __global__ __launch_bounds__(64 * W) void kv8_join_kernel(AttArgs a) {
         count = min(16, x.rows - row0);
         if (parts < 2 || count <= 0) return;
         q0 = x.s.q0;
-        slot0 = part_slot(a, pair / a.c.heads, head, 0) + sub0;
+        slot0 = part_slot<R>(a, pair / a.c.heads, head, 0) + sub0;
         slot1 = slot0 + NEXT;
     } else {
         const int block = blockIdx.x / (R / 16);
@@ -805,20 +807,21 @@ __device__ __forceinline__ int lds_piece(int r, int p) {
     return W * r + (p ^ (W == 16 ? r & 15 : (r >> 1) & 7));
 }
 
-// Many query rows: a block has 128 of them, 32 a wave, and all its waves walk the same keys.
-// A tile is widened once a block on its way into LDS (two tiles in turn: the next one is
-// loaded while this one is used, one barrier a tile).  A key lies at row 16 j + 4 a + b of the
+// Many query rows: a block has 64 or 128 of them, 16 or 32 a wave, and all its waves walk the
+// same keys.  A tile is widened once a block on its way into LDS (two tiles in turn: the next one
+// is loaded while this one is used, one barrier a tile).  A key lies at row 16 j + 4 a + b of the
 // tile for key 16 a + 4 j + b, so that the 16 rows of a sub-tile follow each other; tokens
 // 16 g + 8 e .. + 7 of a value column are its piece 4 e + g.  Two blocks share a CU and are not
 // in step, so one's matrix work meets the other's vector work (one block of 256 rows, whose
 // waves pass the barrier together, was 5 % faster on 4096 of 16384 tokens and 15 to 30 %
-// slower on prompts of 2000).  The loop is near three limits at once, matrix instructions, LDS
-// reads and vector instructions (about 2100, 2300 and 2800 cycles a tile and CU); reads
-// are issued four ahead of the products that use them, which the compiler does not do itself.
-
-template <int D, bool ONE_PAGE, bool SPLIT>
+// slower on prompts of 2000).  With 128 rows the loop is near three limits at once, matrix
+// instructions, LDS reads and vector instructions (about 2100, 2300 and 2800 cycles a tile and
+// CU); reads are issued four ahead of the products that use them, which the compiler does not do
+// itself.  4096 of 16384 tokens, 32 heads of 128: 1060 us, 909 TFLOP/s.
+template <int D, bool ONE_PAGE, bool SPLIT, bool LSE, int P_QT>
 __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) {
     constexpr int NS = D / 32, NV = D / 16;
+    constexpr int P_ROWS = 16 * P_QT * P_WAVES;
     constexpr int AHEAD = 4;         // fragments read before the product that uses the first
     constexpr int CHUNKS = TILE * D / 16;                   // 16-code pieces of a tile's keys, or values
     __shared__ __attribute__((aligned(16))) uint16_t sk[2][TILE * D];
@@ -826,7 +829,6 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
 
     const int wave = uniform((int)threadIdx.x >> 6);
     const int shift = 31 - __clz(a.c.page_tokens), in_page = a.c.page_tokens - 1;
-    const bool want_lse = a.lse != nullptr;
     // heads fastest, then the context's chunks, then the row tiles of a sequence, the last ones
     // first (causal rows see more the later they are)
     int id = blockIdx.x;
@@ -933,9 +935,9 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
                 for (int i = 0; i < NV; ++i) o[t][i] *= alpha[t];
             }
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int i = 0; i < NV; ++i) {
                 const f16x8 v = __builtin_bit_cast(
                     f16x8, reinterpret_cast<const uint4*>(sv[vbuf])[lds_piece<8>(c, 4 * e + g) + 16 * 8 * i]);
 #pragma unroll
@@ -972,11 +974,12 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
         if (!idle && kt < wspan.top && kt + TILE > wspan.low) {
             f32x4 acc[P_QT][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int i = 0; i < NS; ++i) {
 #pragma unroll
-                for (int t = 0; t < P_QT; ++t) acc[t][j] = f32x4{0, 0, 0, 0};
+                for (int j = 0; j < 4; ++j) {
+                    if (i == 0)
 #pragma unroll
-                for (int i = 0; i < NS; ++i) {
+                        for (int t = 0; t < P_QT; ++t) acc[t][j] = f32x4{0, 0, 0, 0};
                     const bf16x8 k = __builtin_bit_cast(
                         bf16x8, reinterpret_cast<const uint4*>(sk[kbuf])[lds_piece<D / 8>(c, 4 * i + g) + 16 * (D / 8) * j]);
 #pragma unroll
@@ -993,7 +996,7 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
             const bool plain = kt + TILE <= wspan.common && kt >= wspan.high && plain_tile(info);
             if (plain) {
 #pragma unroll
-                for (int t = 0; t < P_QT; ++t) alpha[t] = softmax_plain<ONE_PAGE>(acc[t], info, want_lse, st[t], w[t]);
+                for (int t = 0; t < P_QT; ++t) alpha[t] = softmax_plain<ONE_PAGE>(acc[t], info, LSE, st[t], w[t]);
             } else {
 #pragma unroll
                 for (int t = 0; t < P_QT; ++t)
@@ -1022,9 +1025,9 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
                 *reinterpret_cast<uint2*>(dst + 16 * i) =
                     l == 0.0f ? make_uint2(0, 0) : make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
             }
-            if (want_lse && g == 0) a.lse[tok * a.q_heads + mine.head] = lse_of(st[t].m, l);
+            if (LSE && g == 0) a.lse[tok * a.q_heads + mine.head] = lse_of(st[t].m, l);
         } else {
-            const int64_t slot = part_slot(a, index, head, chunk) + 16 * (P_QT * wave + t) + c;
+            const int64_t slot = part_slot<P_ROWS>(a, index, head, chunk) + 16 * (P_QT * wave + t) + c;
             float* dst = a.part_o + slot * D + 4 * g;
 #pragma unroll
             for (int i = 0; i < NV; ++i) *reinterpret_cast<f32x4*>(dst + 16 * i) = o[t][i] * vtop;
@@ -1033,13 +1036,8 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
     }
 }
 
-// Rows of a block, for sequences of that many: 128, or 16 whose waves split the keys (further row
-// tiles find the keys in the L2 cache: blocks of 32 rows were 5 to 10 % slower on 5 to 16 tokens
-// a sequence).
 template <int N>
 using Size = std::integral_constant<int, N>;
-
-int rows_of_block(int64_t rows) { return rows >= PROMPT_ROWS ? P_ROWS : 16; }
 
 }  // namespace
 
@@ -1052,29 +1050,43 @@ int rows_of_block(int64_t rows) { return rows >= PROMPT_ROWS ? P_ROWS : 16; }
 // launch and pays where pairs would leave blocks idle, by three steps; lengths are uneven as a
 // rule, so contexts of eight steps are dealt however many pairs there are (16 x up to 32 k
 // tokens: 181 us in fixed splits, 115 dealt; 256 x up to 400: 57 us dealt, 34 us a block each).
-// Many rows (a step is 64 keys): one for each pair, or, where that is less than 512, for each
-// chunk of a pair's context, about 1024 in all and no less than six steps a chunk.
+// Many rows (a step is 64 keys), 32 query heads over 8 cache heads of 128 in these times: from 64
+// rows a sequence on (16 tokens, 4 x over 8192: 28.2 us, in 16-row tiles 36.9; 40 rows would gain
+// over 8192, 44.5 and 38.9, and lose over 500, 9.1 and 15.4).  128 rows a block where that gives
+// two blocks a CU, four in contexts below 32 steps, or where few new tokens look back on a long
+// context; else 64, whose steps are shorter but reuse what they read half as often.  With 128 and
+// 64 rows: 500 of 500 tokens 21.5 and 16.4 us, 1024 of 1024 37 and 29, 2 x 1000 of 1000 36 and 29,
+// 2048 of 2048 72 and 72, 2500 of 2500 85 and 101, 16 x 500 of 500 42 and 50, 4 x 128 of 8192
+// 71 and 108, 8 x 24 of 8192 51 and 49.  One block for each pair, or, where pairs are less than
+// two a CU, for each chunk of a pair's context: about 1024 (2048 with 64 rows) in all, no less
+// than six steps a chunk.
 AttentionPlan attention_plan(int64_t B, int64_t max_new, int64_t max_kv, int q_heads, int kv_heads, int head_dim) {
     const int group = q_heads / kv_heads;
+    const int64_t query_rows = max_new * group;
     AttentionPlan p{};
-    p.rows = rows_of_block(max_new * group);
-    p.prompt = p.rows == P_ROWS;
-    p.tiles = (max_new * group + p.rows - 1) / p.rows;
-    const int64_t base = B * kv_heads * p.tiles;
+    p.prompt = query_rows >= PROMPT_ROWS;
+    auto pairs = [&](int rows) { return B * kv_heads * ((query_rows + rows - 1) / rows); };
     if (p.prompt) {
         const int64_t steps = std::max<int64_t>(1, (max_kv + TILE - 1) / TILE);
-        const int64_t chunk = std::max<int64_t>(6, (base * steps + 2 * DEAL_BLOCKS - 1) / (2 * DEAL_BLOCKS));
+        const bool looks_back = query_rows >= 128 && 8 * max_new <= max_kv && pairs(128) * steps >= 4 * DEAL_BLOCKS;
+        p.rows = pairs(128) >= (steps < 32 ? 2 : 1) * DEAL_BLOCKS || looks_back ? 128 : 64;
+        p.tiles = (query_rows + p.rows - 1) / p.rows;
+        const int64_t base = pairs(p.rows), blocks = (p.rows == 128 ? 2 : 4) * DEAL_BLOCKS;
+        const int64_t chunk = std::max<int64_t>(6, (base * steps + blocks - 1) / blocks);
         p.parts = base < DEAL_BLOCKS && 2 * steps > 3 * chunk;
         // a context longer than max_kv is still walked: its last chunk is the longest
         p.chunks = p.parts ? (int)((steps + chunk - 1) / chunk) : 1;
         p.chunk_steps = (int)chunk;
         p.blocks = base * p.chunks;
-        p.join_blocks = p.parts ? base * (P_ROWS / 16) : 0;
-        p.part_rows = p.parts ? base * p.chunks * P_ROWS : 0;
+        p.join_blocks = p.parts ? base * (p.rows / 16) : 0;
+        p.part_rows = p.parts ? base * p.chunks * p.rows : 0;
         return p;
     }
+    p.rows = 16;
+    p.tiles = (query_rows + 15) / 16;
+    const int64_t base = pairs(16);
     const int64_t steps = std::max<int64_t>(1, (max_kv + STEP - 1) / STEP);
-    p.wide = p.rows == 16 && base <= 256 && max_kv <= (base < 64 ? 1024 : 2048);
+    p.wide = base <= 256 && max_kv <= (base < 64 ? 1024 : 2048);
     if (p.wide) {
         p.blocks = base;
         return p;
@@ -1120,20 +1132,31 @@ hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const 
         if (c.head_dim == 64) { if (one) go(Size<64>{}, std::true_type{}); else go(Size<64>{}, std::false_type{}); }
         else { if (one) go(Size<128>{}, std::true_type{}); else go(Size<128>{}, std::false_type{}); }
     };
+    auto with_flag = [](bool flag, auto&& go) { if (flag) go(std::true_type{}); else go(std::false_type{}); };
     with_sizes([&](auto d, auto one) {
         constexpr int D = decltype(d)::value;
         constexpr bool ONE = decltype(one)::value;
-        if (p.prompt && p.parts) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, true>), grid, dim3(64 * P_WAVES), 0, stream, a);
-        else if (p.prompt) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, false>), grid, dim3(64 * P_WAVES), 0, stream, a);
-        else if (p.wide) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false, 2 * WAVES>), grid, dim3(128 * WAVES), 0, stream, a);
-        else if (p.parts) hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, true, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
-        else hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
+        with_flag(p.parts, [&](auto parts) {
+            constexpr bool PARTS = decltype(parts)::value;
+            if (p.prompt) {
+                with_flag(lse != nullptr, [&](auto want) {
+                    constexpr bool LSE = decltype(want)::value;
+                    if (p.rows == 128) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, PARTS, LSE, 2>), grid, dim3(64 * P_WAVES), 0, stream, a);
+                    else hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, PARTS, LSE, 1>), grid, dim3(64 * P_WAVES), 0, stream, a);
+                });
+            } else if (p.wide) {
+                hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, false, 2 * WAVES>), grid, dim3(128 * WAVES), 0, stream, a);
+            } else {
+                hipLaunchKernelGGL((kv8_attention_kernel<D, ONE, PARTS, WAVES>), grid, dim3(64 * WAVES), 0, stream, a);
+            }
+        });
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !p.parts) return e;
     with_sizes([&](auto d, auto) {
         constexpr int D = decltype(d)::value;
-        if (p.prompt) hipLaunchKernelGGL((kv8_join_kernel<D, true, P_ROWS, 4>), join, dim3(256), 0, stream, a);
+        if (p.rows == 128) hipLaunchKernelGGL((kv8_join_kernel<D, true, 128, 4>), join, dim3(256), 0, stream, a);
+        else if (p.rows == 64) hipLaunchKernelGGL((kv8_join_kernel<D, true, 64, 4>), join, dim3(256), 0, stream, a);
         else hipLaunchKernelGGL((kv8_join_kernel<D, false, 16, 8>), join, dim3(512), 0, stream, a);
     });
     return hipGetLastError();

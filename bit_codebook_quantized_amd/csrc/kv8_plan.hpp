@@ -7,7 +7,7 @@
 namespace w4a8 {
 
 struct AttentionPlan {
-    int rows;                 // query rows of a block: 128 (many) or 16
+    int rows;                 // query rows of a block: 128 or 64 (many), or 16
     bool prompt;              // many query rows a sequence
     int64_t tiles;            // row tiles of a sequence
     bool wide;                // few rows, short contexts: blocks of 8 waves, a context each
