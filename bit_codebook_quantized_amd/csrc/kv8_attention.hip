@@ -817,17 +817,24 @@ __device__ __forceinline__ int lds_piece(int r, int p) {
 // slower on prompts of 2000).  With 128 rows the loop is near three limits at once, matrix
 // instructions, LDS reads and vector instructions (about 2100, 2300 and 2800 cycles a tile and
 // CU); reads are issued four ahead of the products that use them, which the compiler does not do
-// itself.  4096 of 16384 tokens, 32 heads of 128: 1060 us, 909 TFLOP/s.
-template <int D, bool ONE_PAGE, bool SPLIT, bool LSE, int P_QT>
-__global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) {
+// itself.  4096 of 16384 tokens, 32 heads of 128: 1060 us, 909 TFLOP/s.  With 64 rows it is bound
+// by one step's chain of latencies, barrier to barrier: with HALVES = 2 waves 4 to 7 take every
+// second tile, beside the others, and the two results are added in LDS at the end.
+template <int D, bool ONE_PAGE, bool SPLIT, bool LSE, int P_QT, int HALVES = 1>
+__global__ __launch_bounds__(64 * P_WAVES * HALVES, 2) void kv8_prompt_kernel(AttArgs a) {
+    static_assert(HALVES == 1 || (HALVES == 2 && !SPLIT && P_QT == 1), "halves of a whole context");
     constexpr int NS = D / 32, NV = D / 16;
     constexpr int P_ROWS = 16 * P_QT * P_WAVES;
     constexpr int AHEAD = 4;         // fragments read before the product that uses the first
     constexpr int CHUNKS = TILE * D / 16;                   // 16-code pieces of a tile's keys, or values
-    __shared__ __attribute__((aligned(16))) uint16_t sk[2][TILE * D];
-    __shared__ __attribute__((aligned(16))) uint16_t sv[2][D * TILE];
+    constexpr int STRIDE = HALVES * TILE;                   // from a wave's tile to its next one
+    __shared__ __attribute__((aligned(16))) uint16_t sk_all[HALVES][2][TILE * D];
+    __shared__ __attribute__((aligned(16))) uint16_t sv_all[HALVES][2][D * TILE];
 
-    const int wave = uniform((int)threadIdx.x >> 6);
+    const int half = HALVES == 1 ? 0 : uniform((int)threadIdx.x / (64 * P_WAVES));
+    const int tid = threadIdx.x % (64 * P_WAVES), wave = uniform(tid >> 6);
+    auto& sk = sk_all[half];
+    auto& sv = sv_all[half];
     const int shift = 31 - __clz(a.c.page_tokens), in_page = a.c.page_tokens - 1;
     // heads fastest, then the context's chunks, then the row tiles of a sequence, the last ones
     // first (causal rows see more the later they are)
@@ -842,7 +849,7 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
     const int steps = SPLIT && chunk < a.chunks - 1 ? min(left, a.chunk_steps) : left;
     if (steps <= 0) return;
     const bool all = !SPLIT || steps == x.steps;
-    const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
+    const int lane = tid & 63, c = lane & 15, g = lane >> 4;
     const Seq& s = x.s;
     const Span& span = x.span;
     const int rows = x.rows, row0 = x.row0;
@@ -952,24 +959,25 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
         __builtin_amdgcn_sched_group_barrier(0x008, AHEAD * P_QT, 0);
     };
 
-    if (k0 < k1) {
-        pages(k0);
-        load(k0);
-        pages(k0 + TILE);
+    const int first = k0 + TILE * half;
+    if (first < k1) {
+        pages(first);
+        load(first);
+        pages(first + STRIDE);
         store(0, 0);
     }
     // The queries have arrived: a wait for them inside the loop would wait for the tile that is
     // being fetched as well.
     __builtin_amdgcn_s_waitcnt(0x0F70);      // vmcnt(0)
     int kbuf = 0, vbuf = 0;             // of this tile
-    for (int kt = k0; kt < k1; kt += TILE) {
+    for (int kt = first; kt < k1 + TILE * half; kt += STRIDE) {     // as many steps in both halves
         const int vnext = vbuf ^ 1;
         __syncthreads();
-        const bool more = kt + TILE < k1;
+        const bool more = kt + STRIDE < k1;
         const TileInfo info = tile_info<ONE_PAGE>(ks, vs, a.scale_log2, kt + 16 * g, present);
         if (more) {
-            load(kt + TILE);
-            pages(kt + 2 * TILE);
+            load(kt + STRIDE);
+            pages(kt + 2 * STRIDE);
         }
         if (!idle && kt < wspan.top && kt + TILE > wspan.low) {
             f32x4 acc[P_QT][4];
@@ -1007,6 +1015,31 @@ __global__ __launch_bounds__(64 * P_WAVES, 2) void kv8_prompt_kernel(AttArgs a) 
         if (more) store(kbuf ^ 1, vnext);
         kbuf ^= 1;
         vbuf = vnext;
+    }
+
+    if constexpr (HALVES == 2) {
+        // the second half's results go to the same lanes of the first
+        f32x4* so = reinterpret_cast<f32x4*>(sk_all);
+        float4* sml = reinterpret_cast<float4*>(sv_all);
+        float vtop = __builtin_amdgcn_exp2f(st[0].lv);
+        __syncthreads();
+        if (half == 1) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) so[64 * P_WAVES * i + tid] = o[0][i] * vtop;
+            sml[tid] = make_float4(st[0].m, st[0].l, st[0].lo, 0.0f);
+        }
+        __syncthreads();
+        if (half == 1) return;
+        const float4 other = sml[tid];
+        const float top = __builtin_fmaxf(st[0].m, other.x), ref = top > -__builtin_inff() ? top : 0.0f;
+        const float f0 = __builtin_amdgcn_exp2f(st[0].m - ref), f1 = __builtin_amdgcn_exp2f(other.x - ref);
+        st[0].l = st[0].l * f0 + other.y * f1;
+        st[0].lo = st[0].lo * f0 + other.z * f1;
+        st[0].m = top;
+        st[0].lv = 0.0f;
+        vtop *= f0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) o[0][i] = o[0][i] * vtop + so[64 * P_WAVES * i + tid] * f1;
     }
 
     // lane (c, g) holds columns 16 i + 4 g .. + 3 of its rows
@@ -1059,7 +1092,12 @@ using Size = std::integral_constant<int, N>;
 // 2048 of 2048 72 and 72, 2500 of 2500 85 and 101, 16 x 500 of 500 42 and 50, 4 x 128 of 8192
 // 71 and 108, 8 x 24 of 8192 51 and 49.  One block for each pair, or, where pairs are less than
 // two a CU, for each chunk of a pair's context: about 1024 (2048 with 64 rows) in all, no less
-// than six steps a chunk.
+// than six steps a chunk (64 rows over 16 steps or fewer are not cut, 4 x 64 of 1024: 20.4 us,
+// cut 22.9; 130 of 1500: 22.2, cut 14.2).  Where pairs of 64 rows are up to twice what fits at once with eight
+// waves (two blocks a CU at 64 columns, one at 128), eight waves take every second tile each:
+// the longest chain of steps is half as long (without and with: prompts of 2000 and 125, 16 heads
+// of 64, 55 and 43 us; 1024 of 1024 29.7 and 27.1, 500 of 500 16.5 and 13.7; with more pairs,
+// 2 x 1000 of 1000, 29 and 32, 5 x 500 of 500 21 and 29).
 AttentionPlan attention_plan(int64_t B, int64_t max_new, int64_t max_kv, int q_heads, int kv_heads, int head_dim) {
     const int group = q_heads / kv_heads;
     const int64_t query_rows = max_new * group;
@@ -1073,10 +1111,11 @@ AttentionPlan attention_plan(int64_t B, int64_t max_new, int64_t max_kv, int q_h
         p.tiles = (query_rows + p.rows - 1) / p.rows;
         const int64_t base = pairs(p.rows), blocks = (p.rows == 128 ? 2 : 4) * DEAL_BLOCKS;
         const int64_t chunk = std::max<int64_t>(6, (base * steps + blocks - 1) / blocks);
-        p.parts = base < DEAL_BLOCKS && 2 * steps > 3 * chunk;
+        p.parts = base < DEAL_BLOCKS && (p.rows == 64 ? steps > 16 : 2 * steps > 3 * chunk);
         // a context longer than max_kv is still walked: its last chunk is the longest
         p.chunks = p.parts ? (int)((steps + chunk - 1) / chunk) : 1;
         p.chunk_steps = (int)chunk;
+        p.halves = p.rows == 64 && !p.parts && base <= (head_dim == 64 ? 2 : 1) * DEAL_BLOCKS;
         p.blocks = base * p.chunks;
         p.join_blocks = p.parts ? base * (p.rows / 16) : 0;
         p.part_rows = p.parts ? base * p.chunks * p.rows : 0;
@@ -1142,6 +1181,7 @@ hipError_t launch_attention(const void* q, int q_heads, int64_t q_stride, const 
                 with_flag(lse != nullptr, [&](auto want) {
                     constexpr bool LSE = decltype(want)::value;
                     if (p.rows == 128) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, PARTS, LSE, 2>), grid, dim3(64 * P_WAVES), 0, stream, a);
+                    else if (p.halves) hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, false, LSE, 1, 2>), grid, dim3(128 * P_WAVES), 0, stream, a);
                     else hipLaunchKernelGGL((kv8_prompt_kernel<D, ONE, PARTS, LSE, 1>), grid, dim3(64 * P_WAVES), 0, stream, a);
                 });
             } else if (p.wide) {

@@ -10,6 +10,7 @@ struct AttentionPlan {
     int rows;                 // query rows of a block: 128 or 64 (many), or 16
     bool prompt;              // many query rows a sequence
     int64_t tiles;            // row tiles of a sequence
+    bool halves;              // 64 rows: blocks of 8 waves, every second tile each half
     bool wide;                // few rows, short contexts: blocks of 8 waves, a context each
     bool parts;               // blocks leave partial results, joined by a second launch
     int chunks, chunk_steps;  // many rows: most chunks of a context, steps of 64 keys in one
