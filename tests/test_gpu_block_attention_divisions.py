@@ -10,12 +10,13 @@ from test_gpu_block_attention import Case, say
 
 pytestmark = pytest.mark.gpu
 
-# name: contexts, new tokens, query heads, cache heads
+# name: contexts, new tokens, query heads, cache heads ("64 rows": in blocks of eight waves)
 DIVISIONS = {
     "one launch": ([900, 5, 64], [1, 1, 3], 4, 2),
     "16 rows, a block a pair": ([400, 1, 77, 256] * 10, [1] * 40, 16, 8),
     "16 rows, dealt": ([5001, 17, 3000], [2, 1, 5], 4, 2),
     "64 rows": ([130, 300, 64], [130, 17, 64], 8, 2),
+    "64 rows, many pairs": ([200, 60, 131, 64] * 10, [60, 60, 17, 1] * 10, 32, 8),
     "64 rows in chunks": ([4001, 100, 2000], [20, 17, 33], 8, 2),
     "128 rows": ([2100, 65], [2100, 65], 32, 32),
     "128 rows in chunks": ([2113, 200, 1500, 2049], [130, 128, 1, 260], 8, 8),
