@@ -306,11 +306,14 @@ __device__ __forceinline__ Row row_of(const AttArgs& a, const Seq& s, int kv_hea
     return x;
 }
 
-// Page of token `at` of a sequence (the index is bounded by its length first), -1 if it is
-// not a page of the cache.
+// Table entry of token `at` of a sequence (the index is bounded by its length first).
+__device__ __forceinline__ int entry_at(const int32_t* table, int at, int len, int shift) {
+    return table[(at < len ? at : len - 1) >> shift];
+}
+// The page that an entry names, -1 if it is not a page of the cache.
+__device__ __forceinline__ int page_of(const AttArgs& a, int p) { return p >= 0 && p < a.c.pages ? p : -1; }
 __device__ __forceinline__ int page_at(const AttArgs& a, const int32_t* table, int at, int len, int shift) {
-    const int p = table[(at < len ? at : len - 1) >> shift];
-    return p >= 0 && p < a.c.pages ? p : -1;
+    return page_of(a, entry_at(table, at, len, shift));
 }
 
 __device__ __forceinline__ float lse_of(float m, float l) {
@@ -878,44 +881,42 @@ __global__ __launch_bounds__(64 * P_WAVES * HALVES, 2) void kv8_prompt_kernel(At
         for (int i = 0; i < NV; ++i) o[t][i] = f32x4{0, 0, 0, 0};
     }
 
-    // This thread's pieces of the staged tile: 16 codes of a key, and 16 of a value column.
+    // This thread's pieces of the staged tile: 16 codes of a key, and 16 of a value column.  A
+    // wave has 16 tokens' keys, so one page's; and their values, where a tile has several pages
+    // (with one page neighbouring threads read a column's 64 tokens instead).
     constexpr int NP = CHUNKS / (64 * P_WAVES);
     static_assert(NP * 64 * P_WAVES == CHUNKS, "whole pieces a thread");
-    auto piece_key = [&](int p) { return (tid + 64 * P_WAVES * p) / (D / 16); };
-    auto piece_dim = [&](int p) { return 16 * ((tid + 64 * P_WAVES * p) % (D / 16)); };
-    auto piece_col = [&](int p) { return (tid + 64 * P_WAVES * p) >> 2; };
-    const int stok = 16 * (tid & 3);
+    static_assert(P_WAVES * 16 == TILE, "16 tokens a wave");
+    auto piece_key = [&](int p) { return 16 * wave + (lane + 64 * p) / (D / 16); };
+    auto piece_dim = [&](int p) { return 16 * (lane % (D / 16)); };
+    auto piece_col = [&](int p) { return ONE_PAGE ? (tid + 64 * P_WAVES * p) >> 2 : lane + 64 * p; };
+    const int stok = 16 * (ONE_PAGE ? tid & 3 : wave);
     uint4 kw[NP], vw[NP];
-    // Page numbers are fetched a tile before what they point at: of the staged piece's keys and
-    // values, and (for the scales) of this lane's 16 tokens.
-    int pk[NP] = {}, pv = 0, ps = 0;
+    // Page numbers are fetched a tile before what they point at, and first looked at there (a
+    // look at once would wait for the tile's loads before them): of the staged pieces, and (for
+    // the scales) of this lane's 16 tokens.
+    int entry = 0, scale_entry = 0;
     auto pages = [&](int kt) {
-        if constexpr (ONE_PAGE) {
-            pv = ps = uniform(page_at(a, table, kt, s.len, shift));
-#pragma unroll
-            for (int p = 0; p < NP; ++p) pk[p] = pv;
-        } else {
-#pragma unroll
-            for (int p = 0; p < NP; ++p) pk[p] = page_at(a, table, kt + piece_key(p), s.len, shift);
-            pv = page_at(a, table, kt + stok, s.len, shift);
-            ps = page_at(a, table, kt + 16 * g, s.len, shift);
-        }
+        entry = entry_at(table, ONE_PAGE ? kt : kt + 16 * wave, s.len, shift);
+        if constexpr (!ONE_PAGE) scale_entry = entry_at(table, kt + 16 * g, s.len, shift);
     };
     float ks = 0.0f, vs = 0.0f;        // of the tile that is loaded
     bool present = false;
     auto load = [&](int kt) {
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            const int8_t* page = a.c.k + ((((int64_t)(pk[p] < 0 ? 0 : pk[p]) * a.c.heads + head) << shift)) * D;
-            kw[p] = *reinterpret_cast<const uint4*>(page + ((kt + piece_key(p)) & in_page) * D + piece_dim(p));
-        }
-        const int8_t* values = a.c.v + (((int64_t)(pv < 0 ? 0 : pv) * a.c.heads + head) << shift) * D;
+        const int pp = page_of(a, uniform(entry)), ps = ONE_PAGE ? pp : page_of(a, scale_entry);
+        const int64_t page = (((int64_t)(pp < 0 ? 0 : pp) * a.c.heads + head) << shift) * D;
+        const int8_t* keys = a.c.k + page;
+        const int8_t* values = a.c.v + page;
 #pragma unroll
         for (int p = 0; p < NP; ++p)
-            vw[p] = *reinterpret_cast<const uint4*>(values + (piece_col(p) << shift) + ((kt + stok) & in_page));
-        const int64_t page = (int64_t)(ps < 0 ? 0 : ps) * a.c.heads + head;
-        ks = a.c.k_scale[page];
-        vs = a.c.v_scale[page];
+            kw[p] = *reinterpret_cast<const uint4*>(keys + (uint32_t)(((kt + piece_key(p)) & in_page) * D + piece_dim(p)));
+#pragma unroll
+        for (int p = 0; p < NP; ++p)
+            vw[p] = *reinterpret_cast<const uint4*>(values + (uint32_t)((piece_col(p) << shift) + ((kt + stok) & in_page)));
+        // byte offsets in 32 bits: a page and head has 2048 codes or more, so the card holds fewer than 2^28
+        const uint32_t at = 4u * ((uint32_t)(ps < 0 ? 0 : ps) * (uint32_t)a.c.heads + (uint32_t)head);
+        ks = *reinterpret_cast<const float*>(reinterpret_cast<const char*>(a.c.k_scale) + at);
+        vs = *reinterpret_cast<const float*>(reinterpret_cast<const char*>(a.c.v_scale) + at);
         present = ps >= 0;
     };
     auto store = [&](int kbuf, int vbuf) {
