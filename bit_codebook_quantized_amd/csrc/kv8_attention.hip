@@ -312,9 +312,6 @@ __device__ __forceinline__ int entry_at(const int32_t* table, int at, int len, i
 }
 // The page that an entry names, -1 if it is not a page of the cache.
 __device__ __forceinline__ int page_of(const AttArgs& a, int p) { return p >= 0 && p < a.c.pages ? p : -1; }
-__device__ __forceinline__ int page_at(const AttArgs& a, const int32_t* table, int at, int len, int shift) {
-    return page_of(a, entry_at(table, at, len, shift));
-}
 
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l) - W_EXP) * 0.69314718055994531f;
@@ -572,18 +569,17 @@ __global__ __launch_bounds__(64 * W, 2) void kv8_attention_kernel(AttArgs a) {
 
         // lane (c, g): keys from row c of a sub-tile (tokens 16 (c / 4) + 4 j + c % 4), 16 codes
         // of every 64; values of tokens 16 g .. 16 g + 15.  Page numbers are fetched a step
-        // before what they point at.
+        // before what they point at, and first looked at there (a look at once would wait for
+        // the loads before them).
         uint4 kw[4 * NK];
-        int pk = 0, pv = 0;
+        int entry_k = 0, entry_v = 0, pk = 0, pv = 0;
         auto pages = [&](int kt) {
-            if constexpr (ONE_PAGE) {
-                pk = pv = uniform(page_at(a, table, uniform(kt), s.len, shift));
-            } else {
-                pk = page_at(a, table, kt + 16 * (c >> 2), s.len, shift);
-                pv = page_at(a, table, kt + 16 * g, s.len, shift);
-            }
+            entry_k = entry_at(table, ONE_PAGE ? uniform(kt) : kt + 16 * (c >> 2), s.len, shift);
+            if constexpr (!ONE_PAGE) entry_v = entry_at(table, kt + 16 * g, s.len, shift);
         };
         auto load_keys = [&](int kt) {
+            pk = page_of(a, ONE_PAGE ? uniform(entry_k) : entry_k);
+            pv = ONE_PAGE ? pk : page_of(a, entry_v);
             const int8_t* kp = a.c.k + ((((int64_t)(pk < 0 ? 0 : pk) * a.c.heads + head) << shift) +
                                         ((kt + 16 * (c >> 2)) & in_page) + (c & 3)) * D + 16 * g;
 #pragma unroll
@@ -600,11 +596,11 @@ __global__ __launch_bounds__(64 * W, 2) void kv8_attention_kernel(AttArgs a) {
             const int8_t* vp = a.c.v + ((vpage * D) << shift) + ((int64_t)c << shift) + ((kt + 16 * g) & in_page);
             const float ks = a.c.k_scale[vpage], vs = a.c.v_scale[vpage];
             const bool present = pv >= 0;
+            const bool more = kt + STEP < k1;
+            if (more) pages(kt + STEP);
             uint4 vw[NV];
 #pragma unroll
             for (int i = 0; i < NV; ++i) vw[i] = *reinterpret_cast<const uint4*>(vp + ((int64_t)(16 * i) << shift));
-            const bool more = kt + STEP < k1;
-            if (more) pages(kt + STEP);
 
             f32x4 acc[4];
 #pragma unroll
