@@ -816,7 +816,7 @@ __device__ __forceinline__ int lds_piece(int r, int p) {
 // slower on prompts of 2000).  With 128 rows the loop is near three limits at once, matrix
 // instructions, LDS reads and vector instructions (about 2100, 2300 and 2800 cycles a tile and
 // CU); reads are issued four ahead of the products that use them, which the compiler does not do
-// itself.  4096 of 16384 tokens, 32 heads of 128: 1060 us, 909 TFLOP/s.  With 64 rows it is bound
+// itself.  4096 of 16384 tokens, 32 heads of 128: 991 us, 971 TFLOP/s.  With 64 rows it is bound
 // by one step's chain of latencies, barrier to barrier: with HALVES = 2 waves 4 to 7 take every
 // second tile, beside the others, and the two results are added in LDS at the end.
 template <int D, bool ONE_PAGE, bool SPLIT, bool LSE, int P_QT, int HALVES = 1>
@@ -1073,7 +1073,7 @@ using Size = std::integral_constant<int, N>;
 
 // Blocks of a launch.
 // Few rows, short contexts, few of them: a block of 8 waves for each pair, no parts (1 x 1000
-// tokens, 8 cache heads: 11.6 us against 11.9 and a launch more; 1 x 2048: 16.4 against 12.5;
+// tokens, 8 cache heads: 11.3 us against 11.9 and a launch more; 1 x 2048: 16.4 against 12.5;
 // 16 x up to 2048: 17.7 against 20.8; 16 x up to 4096: 28.1 against 27.5).
 // Few rows otherwise (a step is 256 keys): one for each (row tile, head), or 512 (two a CU, as many as fit
 // at once) that share all steps equally and whose parts are then joined.  Dealing costs a second
@@ -1081,20 +1081,20 @@ using Size = std::integral_constant<int, N>;
 // rule, so contexts of eight steps are dealt however many pairs there are (16 x up to 32 k
 // tokens: 181 us in fixed splits, 115 dealt; 256 x up to 400: 57 us dealt, 34 us a block each).
 // Many rows (a step is 64 keys), 32 query heads over 8 cache heads of 128 in these times: from 64
-// rows a sequence on (16 tokens, 4 x over 8192: 28.2 us, in 16-row tiles 36.9; 40 rows would gain
-// over 8192, 44.5 and 38.9, and lose over 500, 9.1 and 15.4).  128 rows a block where that gives
-// two blocks a CU, four in contexts below 32 steps, or where few new tokens look back on a long
+// rows a sequence on (4 x 16 tokens of 8192: 27 us, in 16-row tiles 38; 40 rows would gain over
+// 8192, 45 and 35, and lose over 500, 9.1 and 12.3).  128 rows a block where that gives two
+// blocks a CU, four in contexts below 32 steps, or where few new tokens look back on a long
 // context; else 64, whose steps are shorter but reuse what they read half as often.  With 128 and
-// 64 rows: 500 of 500 tokens 21.5 and 16.4 us, 1024 of 1024 37 and 29, 2 x 1000 of 1000 36 and 29,
-// 2048 of 2048 72 and 72, 2500 of 2500 85 and 101, 16 x 500 of 500 42 and 50, 4 x 128 of 8192
-// 71 and 108, 8 x 24 of 8192 51 and 49.  One block for each pair, or, where pairs are less than
+// 64 rows: 500 of 500 tokens 20.7 and 13.3 us, 1024 of 1024 36 and 26, 2 x 1000 of 1000 35 and 27,
+// 2048 of 2048 66 and 68, 2500 of 2500 80 and 94, 16 x 500 of 500 41 and 48, 4 x 128 of 8192
+// 66 and 75, 8 x 24 of 8192 46.8 and 45.8.  One block for each pair, or, where pairs are less than
 // two a CU, for each chunk of a pair's context: about 1024 (2048 with 64 rows) in all, no less
-// than six steps a chunk (64 rows over 16 steps or fewer are not cut, 4 x 64 of 1024: 20.4 us,
-// cut 22.9; 130 of 1500: 22.2, cut 14.2).  Where pairs of 64 rows are up to twice what fits at once with eight
-// waves (two blocks a CU at 64 columns, one at 128), eight waves take every second tile each:
-// the longest chain of steps is half as long (without and with: prompts of 2000 and 125, 16 heads
-// of 64, 55 and 43 us; 1024 of 1024 29.7 and 27.1, 500 of 500 16.5 and 13.7; with more pairs,
-// 2 x 1000 of 1000, 29 and 32, 5 x 500 of 500 21 and 29).
+// than six steps a chunk (64 rows over 16 steps or fewer are not cut, 4 x 64 of 1024: 19.6 us,
+// cut 22.2; 130 of 1500: 20.1, cut 13.3).  Where pairs of 64 rows are up to twice what fits at
+// once with eight waves (two blocks a CU at 64 columns, one at 128), eight waves take every second
+// tile each: the longest chain of steps is half as long (without and with: prompts of 2000 and
+// 125, 16 heads of 64, 48 and 42 us; 1024 of 1024 28 and 27, 500 of 500 15.1 and 13.3; with more
+// pairs, 2 x 1000 of 1000, 27 and 31, 5 x 500 of 500 21 and 29).
 AttentionPlan attention_plan(int64_t B, int64_t max_new, int64_t max_kv, int q_heads, int kv_heads, int head_dim) {
     const int group = q_heads / kv_heads;
     const int64_t query_rows = max_new * group;
