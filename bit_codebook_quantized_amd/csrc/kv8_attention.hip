@@ -131,6 +131,10 @@ struct RowState {
 };
 __device__ __forceinline__ RowState fresh_row() { return RowState{-__builtin_inff(), 0.0f, 0.0f, -__builtin_inff()}; }
 
+// The square root of a row's largest value scale: results take it twice, so that the scale may be
+// subnormal, or so small that dividing it by the sum would make it so.
+__device__ __forceinline__ float half_scale(const RowState& s) { return __builtin_amdgcn_exp2f(0.5f * s.lv); }
+
 // Maximum and sum over the four lane groups of a row (lanes c, c + 16, c + 32, c + 48).
 __device__ __forceinline__ float group_max(float v) {
     const uint32_t u = __float_as_uint(v);
@@ -154,7 +158,8 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 // What a lane knows of a tile: its 16 keys start at `key`, they are in one page.
 struct TileInfo {
     float fk, fv;         // key scale times scale_log2, value scale
-    float lfv, lvmax;     // log2 of fv, and the largest of the tile's pages (NaN left out)
+    float lfv, lvmax;     // log2 of fv (-inf below the smallest normal number), and the largest of the
+                          // tile's pages (NaN left out)
     int key;
     bool present;         // the page exists
 };
@@ -238,6 +243,7 @@ __device__ __forceinline__ float softmax_any(const f32x4 (&acc)[4], const TileIn
     float x[16];
     float top = -__builtin_inff();
     bool any = false;
+    const float lfv = __builtin_log2f(t.fv);       // of subnormal scales too
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
         const int key = t.key + j;
@@ -246,12 +252,12 @@ __device__ __forceinline__ float softmax_any(const f32x4 (&acc)[4], const TileIn
         top = __builtin_fmaxf(top, x[j]);
         any |= seen;
     }
-    const float lvn = group_max(__builtin_fmaxf(s.lv, any ? t.lfv : -__builtin_inff()));
+    const float lvn = group_max(__builtin_fmaxf(s.lv, any ? lfv : -__builtin_inff()));
     const float mn = __builtin_fmaxf(s.m, group_max(top));
     const float ref = mn > -__builtin_inff() ? mn : 0.0f;          // a row that has seen no key yet
     const float alpha = __builtin_amdgcn_exp2f(s.m - ref);
     const float alpha_o = s.lv == lvn ? alpha : alpha * __builtin_amdgcn_exp2f(s.lv - lvn);
-    const float r = t.lfv > -__builtin_inff() ? __builtin_amdgcn_exp2f(t.lfv - lvn) : t.fv;
+    const float r = lfv > -__builtin_inff() ? __builtin_amdgcn_exp2f(lfv - lvn) : t.fv;
     float sum = 0.0f, rounded = 0.0f;
     uint32_t pw[8];
 #pragma unroll
@@ -629,12 +635,12 @@ __global__ __launch_bounds__(64 * W, 2) void kv8_attention_kernel(AttArgs a) {
                 o[i] = mfma(widen_f16(vw[i].z, vw[i].w), w.hi, o[i]);
             }
         }
-        const float vtop = __builtin_amdgcn_exp2f(st.lv);
+        const float vhalf = half_scale(st);
         if (g == 0) { sm[wave][c] = st.m; sl[wave][c] = st.l; slo[wave][c] = st.lo; }
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) so[wave][16 * i + 4 * g + e][c] = o[i][e] * vtop;
+            for (int e = 0; e < 4; ++e) so[wave][16 * i + 4 * g + e][c] = o[i][e] * vhalf * vhalf;
         __syncthreads();
 
         // join the waves: 4 W threads a row
@@ -1018,11 +1024,11 @@ __global__ __launch_bounds__(64 * P_WAVES * HALVES, 2) void kv8_prompt_kernel(At
         // the second half's results go to the same lanes of the first
         f32x4* so = reinterpret_cast<f32x4*>(sk_all);
         float4* sml = reinterpret_cast<float4*>(sv_all);
-        float vtop = __builtin_amdgcn_exp2f(st[0].lv);
+        const float vhalf = half_scale(st[0]);
         __syncthreads();
         if (half == 1) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) so[64 * P_WAVES * i + tid] = o[0][i] * vtop;
+            for (int i = 0; i < NV; ++i) so[64 * P_WAVES * i + tid] = o[0][i] * vhalf * vhalf;
             sml[tid] = make_float4(st[0].m, st[0].l, st[0].lo, 0.0f);
         }
         __syncthreads();
@@ -1034,24 +1040,23 @@ __global__ __launch_bounds__(64 * P_WAVES * HALVES, 2) void kv8_prompt_kernel(At
         st[0].lo = st[0].lo * f0 + other.z * f1;
         st[0].m = top;
         st[0].lv = 0.0f;
-        vtop *= f0;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) o[0][i] = o[0][i] * vtop + so[64 * P_WAVES * i + tid] * f1;
+        for (int i = 0; i < NV; ++i) o[0][i] = o[0][i] * vhalf * vhalf * f0 + so[64 * P_WAVES * i + tid] * f1;
     }
 
     // lane (c, g) holds columns 16 i + 4 g .. + 3 of its rows
 #pragma unroll
     for (int t = 0; t < P_QT; ++t) {
-        const float l = st[t].l, lo = st[t].lo, vtop = __builtin_amdgcn_exp2f(st[t].lv);
+        const float l = st[t].l, lo = st[t].lo, vhalf = half_scale(st[t]);
         if (wrow0 + 16 * t + c >= rows) continue;
         const Row mine = row_of(a, s, head, wrow0 + 16 * t + c, rows);
         const int64_t tok = s.q0 + mine.token;
         if (all) {
-            const float inv = l == 0.0f ? 0.0f : vtop / lo;
+            const float inv = l == 0.0f ? 0.0f : vhalf / lo;
             uint16_t* dst = a.out + tok * a.out_stride + (int64_t)mine.head * D + 4 * g;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const f32x4 v = o[t][i] * inv;
+                const f32x4 v = o[t][i] * vhalf * inv;
                 *reinterpret_cast<uint2*>(dst + 16 * i) =
                     l == 0.0f ? make_uint2(0, 0) : make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
             }
@@ -1060,7 +1065,7 @@ __global__ __launch_bounds__(64 * P_WAVES * HALVES, 2) void kv8_prompt_kernel(At
             const int64_t slot = part_slot<P_ROWS>(a, index, head, chunk) + 16 * (P_QT * wave + t) + c;
             float* dst = a.part_o + slot * D + 4 * g;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) *reinterpret_cast<f32x4*>(dst + 16 * i) = o[t][i] * vtop;
+            for (int i = 0; i < NV; ++i) *reinterpret_cast<f32x4*>(dst + 16 * i) = o[t][i] * vhalf * vhalf;
             if (g == 0) *reinterpret_cast<float4*>(a.part_ml + slot * 4) = make_float4(st[t].m, l, lo, 0.0f);
         }
     }
