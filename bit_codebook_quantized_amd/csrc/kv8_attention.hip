@@ -175,8 +175,13 @@ __device__ __forceinline__ TileInfo tile_info(float k_scale, float v_scale, floa
     t.present = present;
     return t;
 }
-// Whether the tile needs no care: every page exists and has a positive value scale.
-__device__ __forceinline__ bool plain_tile(const TileInfo& t) { return __all(t.present && t.lfv > -__builtin_inff()); }
+// Whether the tile needs no care: every page exists, has a positive value scale, and none of its
+// value scales is below 2^-8 of the largest that the rows (lv) and the tile have met.  A weight then
+// loses at most 2^-32 of the largest one to fp16's smallest step, in the sum as well.
+template <bool ONE_PAGE>
+__device__ __forceinline__ bool plain_tile(const TileInfo& t, float lv) {
+    return __all(t.present && t.lfv > (ONE_PAGE ? lv : __builtin_fmaxf(lv, t.lvmax)) - 8.0f);
+}
 
 struct Weights {
     f16x8 lo, hi;         // of this lane's tokens 0 .. 7 and 8 .. 15
@@ -237,7 +242,9 @@ __device__ __forceinline__ float softmax_plain(const f32x4 (&acc)[4], const Tile
 // The same for any tile.  Few keys may count in one that is partly masked, so the sum that
 // divides the result is taken of the weights as rounded (the rounding of a row with one key
 // cancels, of few nearly), and the one for lse before; and a masked weight times a NaN scale
-// must not reach the product.
+// must not reach the product.  A weight that the value scale brings below fp16's normal numbers
+// counts in that sum as it was before the rounding, and so do all weights of a page whose scale
+// leaves none above them: such keys add little or nothing to the product, but divide it like any other.
 __device__ __forceinline__ float softmax_any(const f32x4 (&acc)[4], const TileInfo& t, int begin, int end, RowState& s,
                                              Weights& wt) {
     float x[16];
@@ -267,8 +274,9 @@ __device__ __forceinline__ float softmax_any(const f32x4 (&acc)[4], const TileIn
         for (int e = 0; e < 2; ++e) {
             const float p = __builtin_amdgcn_exp2f(x[2 * j + e] - ref + W_EXP);
             sum += p;
-            w[e] = (_Float16)(p == 0.0f ? 0.0f : p * r);
-            rounded += (float)w[e];
+            const float scaled = p == 0.0f ? 0.0f : p * r;
+            w[e] = (_Float16)scaled;
+            rounded += scaled >= 0x1p-14f ? (float)w[e] : scaled;
         }
         pw[j] = __builtin_bit_cast(uint32_t, w);
     }
@@ -276,7 +284,7 @@ __device__ __forceinline__ float softmax_any(const f32x4 (&acc)[4], const TileIn
     s.m = mn;
     s.lv = lvn;
     s.l = __builtin_fmaf(s.l, alpha, group_sum(sum));
-    s.lo = __builtin_fmaf(s.lo, alpha, group_sum(any && r > 0.0f ? rounded / r : sum));
+    s.lo = __builtin_fmaf(s.lo, alpha, group_sum(any && r > 0x1p-29f ? rounded / r : sum));
     return alpha_o;
 }
 
@@ -621,7 +629,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv8_attention_kernel(AttArgs a) {
             }
             if (more) load_keys(kt + STEP);
             const TileInfo t = tile_info<ONE_PAGE>(ks, vs, a.scale_log2, kt + 16 * g, present);
-            const bool plain = kt + TILE <= span.common && kt >= span.high && plain_tile(t);
+            const bool plain = kt + TILE <= span.common && kt >= span.high && plain_tile<ONE_PAGE>(t, st.lv);
             Weights w;
             const float alpha = plain ? softmax_plain<ONE_PAGE>(acc, t, want_lse, st, w)
                                       : softmax_any(acc, t, row.begin, row.end, st, w);
@@ -1004,7 +1012,8 @@ __global__ __launch_bounds__(64 * P_WAVES * HALVES, 2) void kv8_prompt_kernel(At
                 __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);
             }
             __builtin_amdgcn_sched_group_barrier(0x008, AHEAD * P_QT, 1);
-            const bool plain = kt + TILE <= wspan.common && kt >= wspan.high && plain_tile(info);
+            const bool plain = kt + TILE <= wspan.common && kt >= wspan.high &&
+                               plain_tile<ONE_PAGE>(info, P_QT == 1 ? st[0].lv : __builtin_fmaxf(st[0].lv, st[P_QT - 1].lv));
             if (plain) {
 #pragma unroll
                 for (int t = 0; t < P_QT; ++t) alpha[t] = softmax_plain<ONE_PAGE>(acc[t], info, LSE, st[t], w[t]);

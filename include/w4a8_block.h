@@ -185,8 +185,10 @@ int kv8_append(const w4a8_kv8* cache, const int32_t* ctx_len, const int32_t* q_s
  * A row that sees no key gets out 0 and lse -inf.  Codes are exact in bf16, and so are the
  * queries: scores are exact products summed in fp32; the weights, relative to the largest
  * seen so far (as is the value scale), are rounded to fp16 (11 bits; below 2^-29 of the
- * largest in steps of 2^-39) for the product with the values, which sums in fp32; out is
- * rounded once to bf16.  A masked key or value never reaches the result, whatever it holds.
+ * largest in steps of 2^-39) for the product with the values, which sums in fp32.  The
+ * sum of the weights is in fp32 and independent of value scales: of the weights as rounded
+ * where fp16 holds them to 11 bits (that rounding then nearly cancels), else unrounded.
+ * out is rounded once to bf16.  A masked key or value never reaches the result, whatever it holds.
  *
  *   q            in   bf16 bits, T tokens of q_heads heads, q_stride elements apart
  *   q_heads           multiple of cache->heads
