@@ -242,7 +242,7 @@ __device__ __forceinline__ float softmax_plain(const f32x4 (&acc)[4], const Tile
 // The same for any tile.  Few keys may count in one that is partly masked, so the sum that
 // divides the result is taken of the weights as rounded (the rounding of a row with one key
 // cancels, of few nearly), and the one for lse before; and a masked weight times a NaN scale
-// must not reach the product.  A weight that the value scale brings below fp16's normal numbers
+// must not reach the product, but one that is seen must, also where the weight has vanished.  A weight that the value scale brings below fp16's normal numbers
 // counts in that sum as it was before the rounding, and so do all weights of a page whose scale
 // leaves none above them: such keys add little or nothing to the product, but divide it like any other.
 __device__ __forceinline__ float softmax_any(const f32x4 (&acc)[4], const TileInfo& t, int begin, int end, RowState& s,
@@ -274,7 +274,7 @@ __device__ __forceinline__ float softmax_any(const f32x4 (&acc)[4], const TileIn
         for (int e = 0; e < 2; ++e) {
             const float p = __builtin_amdgcn_exp2f(x[2 * j + e] - ref + W_EXP);
             sum += p;
-            const float scaled = p == 0.0f ? 0.0f : p * r;
+            const float scaled = x[2 * j + e] == -__builtin_inff() ? 0.0f : p * r;
             w[e] = (_Float16)scaled;
             rounded += scaled >= 0x1p-14f ? (float)w[e] : scaled;
         }

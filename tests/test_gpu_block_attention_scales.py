@@ -95,3 +95,16 @@ def test_one_loud_key_over_many_quiet_ones(new, quiet_first):
     c.vs[:], c.vs[loud] = 2.0 ** -34, 2.0 ** -6
     c.q.fill_(9.7 / 128 ** 0.5)
     check_far(c)
+
+
+@pytest.mark.parametrize("name", DIVISIONS)
+def test_a_poisoned_page_counts_however_small_its_weights(name):
+    """Rows that see a page of NaN values are NaN, also where its weights vanish.  lse does not depend on values, but
+    rounds the scores near the largest, and so near itself, in another place: a few 2^-23 of it."""
+    say(name)
+    c = case(name, 64, 16, seed=4, q_scale=30.0)
+    _, lse0, _ = c.run()
+    c.vs[c.table[:, 0]] = np.nan
+    out, lse, _ = c.run()
+    assert np.isnan(out).all()
+    assert (np.abs(lse - lse0) <= 2.0 ** -20 * (1 + np.abs(lse0))).all()
