@@ -177,10 +177,28 @@ __device__ __forceinline__ TileInfo tile_info(float k_scale, float v_scale, floa
 }
 // Whether the tile needs no care: every page exists, has a positive value scale, and none of its
 // value scales is below 2^-8 of the largest that the rows (lv) and the tile have met.  A weight then
-// loses at most 2^-32 of the largest one to fp16's smallest step, in the sum as well.
+// loses at most 2^-32 of the largest one to fp16's smallest step, in the sum as well.  And its key
+// scale is below the rows' limit (score_limit).
 template <bool ONE_PAGE>
-__device__ __forceinline__ bool plain_tile(const TileInfo& t, float lv) {
-    return __all(t.present && t.lfv > (ONE_PAGE ? lv : __builtin_fmaxf(lv, t.lvmax)) - 8.0f);
+__device__ __forceinline__ bool plain_tile(const TileInfo& t, float lv, float limit) {
+    return __all(t.present & (t.lfv > (ONE_PAGE ? lv : __builtin_fmaxf(lv, t.lvmax)) - 8.0f) & (t.fk < limit));
+}
+
+// The factor of scores up to which none of this lane's query row can pass 2^12, whatever the codes
+// are (0 for a row that is not finite).  From there on the exponent's bias in softmax_plain, which
+// holds the maximum, would be off by more than 2^-11, and from 2^23 on by more than fp16 has room for.
+// The sum of |q| comes out of a matrix product in every lane that holds a part of the row.
+template <int N>
+__device__ __forceinline__ float score_limit(const bf16x8 (&q)[N]) {
+    const bf16x8 c = __builtin_bit_cast(bf16x8, make_uint4(0x43004300u, 0x43004300u, 0x43004300u, 0x43004300u));   // 128
+    f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        uint4 w = __builtin_bit_cast(uint4, q[i]);
+        w.x &= 0x7FFF7FFFu; w.y &= 0x7FFF7FFFu; w.z &= 0x7FFF7FFFu; w.w &= 0x7FFF7FFFu;
+        sum = mfma(c, __builtin_bit_cast(bf16x8, w), sum);
+    }
+    return sum[0] <= 3.402823466e38f ? 0x1p12f * __builtin_amdgcn_rcpf(sum[0]) : 0.0f;
 }
 
 struct Weights {
@@ -605,6 +623,7 @@ __global__ __launch_bounds__(64 * W, 2) void kv8_attention_kernel(AttArgs a) {
             pages(k0);
             load_keys(k0);
         }
+        float limit = 0.0f;
         for (int kt = k0; kt < k1; kt += STEP) {
             const int64_t vpage = (int64_t)(pv < 0 ? 0 : pv) * a.c.heads + head;
             const int8_t* vp = a.c.v + ((vpage * D) << shift) + ((int64_t)c << shift) + ((kt + 16 * g) & in_page);
@@ -628,8 +647,9 @@ __global__ __launch_bounds__(64 * W, 2) void kv8_attention_kernel(AttArgs a) {
                 }
             }
             if (more) load_keys(kt + STEP);
+            if (kt == k0) limit = score_limit(qf);      // here, where the first loads are under way
             const TileInfo t = tile_info<ONE_PAGE>(ks, vs, a.scale_log2, kt + 16 * g, present);
-            const bool plain = kt + TILE <= span.common && kt >= span.high && plain_tile<ONE_PAGE>(t, st.lv);
+            const bool plain = kt + TILE <= span.common && kt >= span.high && plain_tile<ONE_PAGE>(t, st.lv, limit);
             Weights w;
             const float alpha = plain ? softmax_plain<ONE_PAGE>(acc, t, want_lse, st, w)
                                       : softmax_any(acc, t, row.begin, row.end, st, w);
@@ -971,10 +991,14 @@ __global__ __launch_bounds__(64 * P_WAVES * HALVES, 2) void kv8_prompt_kernel(At
     };
 
     const int first = k0 + TILE * half;
+    float limit = 0.0f;
     if (first < k1) {
         pages(first);
         load(first);
         pages(first + STRIDE);
+        limit = score_limit(qf[0]);        // here, where the first tile is on its way
+#pragma unroll
+        for (int t = 1; t < P_QT; ++t) limit = __builtin_fminf(limit, score_limit(qf[t]));
         store(0, 0);
     }
     // The queries have arrived: a wait for them inside the loop would wait for the tile that is
@@ -1013,7 +1037,7 @@ __global__ __launch_bounds__(64 * P_WAVES * HALVES, 2) void kv8_prompt_kernel(At
             }
             __builtin_amdgcn_sched_group_barrier(0x008, AHEAD * P_QT, 1);
             const bool plain = kt + TILE <= wspan.common && kt >= wspan.high &&
-                               plain_tile<ONE_PAGE>(info, P_QT == 1 ? st[0].lv : __builtin_fmaxf(st[0].lv, st[P_QT - 1].lv));
+                               plain_tile<ONE_PAGE>(info, P_QT == 1 ? st[0].lv : __builtin_fmaxf(st[0].lv, st[P_QT - 1].lv), limit);
             if (plain) {
 #pragma unroll
                 for (int t = 0; t < P_QT; ++t) alpha[t] = softmax_plain<ONE_PAGE>(acc[t], info, LSE, st[t], w[t]);

@@ -12,9 +12,10 @@ number.  lse moves by ds."""
 
 import numpy as np
 import pytest
+import torch
 
 from block_ref import U, attention, bf16_gap
-from test_gpu_block_attention import Case, say
+from test_gpu_block_attention import DEV, Case, say
 from test_gpu_block_attention_divisions import DIVISIONS, case
 
 pytestmark = pytest.mark.gpu
@@ -108,3 +109,34 @@ def test_a_poisoned_page_counts_however_small_its_weights(name):
     out, lse, _ = c.run()
     assert np.isnan(out).all()
     assert (np.abs(lse - lse0) <= 2.0 ** -20 * (1 + np.abs(lse0))).all()
+
+
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("name", DIVISIONS)
+def test_large_scores(name, D, P):
+    """Scores from 2^12 to 2^27: every key's is one of three, so the result is the mean of the values of the largest."""
+    say(name, D, P)
+    c = case(name, D, P, seed=6)
+    g = np.random.default_rng(5)
+    c.k[:] = g.integers(1, 4, size=c.k.shape[:3])[..., None]
+    c.ks[:] = 1.0
+    c.q = torch.from_numpy(2.0 ** g.integers(6, 19, size=c.q.shape[:2]))[..., None].expand(c.q.shape).to(torch.bfloat16).to(DEV)
+    c.q = c.q.contiguous()
+    out, lse, _ = c.run(scale=1.0)
+    for b, n in enumerate(c.lens):
+        s, m = c.start[b], c.news[b]
+        pid = c.table[b, :-(-n // P)]
+        for hq in range(c.Hq):
+            h = hq // (c.Hq // c.Hkv)
+            k = c.k[pid, h].reshape(-1, D)[:n].astype(np.float64)
+            v = (c.v[pid, h] * c.vs[pid, h].astype(np.float64)[:, None, None]).transpose(0, 2, 1).reshape(-1, D)[:n]
+            for i in (r for r in ROWS if r < m):
+                q = c.q[s + i:s + i + 1, hq].double().cpu().numpy()
+                ref, ls, size = attention(q, k, v, n - m + i, 1.0, True, 0)
+                # scores are exact but for the scale's rounding, the same for all keys
+                bound = (2.0 ** -10 + 2.0 ** -32 * n + 1e-5) * size[0] + 2.0 ** -40 * n * np.abs(v).max()
+                bound = 1.01 * (bound + bf16_gap(ref[0]))
+                err = np.abs(out[s + i, hq] - ref[0])
+                assert (err <= bound).all(), (b, hq, i, (err / bound).max())
+                # the scale times log2(e), the score and lse are rounded to fp32
+                assert abs(lse[s + i, hq] - ls[0]) <= 2.0 ** -21 * abs(ls[0]) + 1e-4
