@@ -100,9 +100,16 @@ int check_batch(int64_t B, int64_t T, int64_t max_new) {
 // No sequence has more new tokens than there are rows.
 int64_t bounded_new(int64_t T, int64_t max_new) { return max_new < T ? max_new : T; }
 
-// The query rows of a batch are within a launch's blocks.
-bool fits(int64_t B, int64_t max_new, int64_t q_heads) {
-    return B <= MAX_BLOCKS && max_new * q_heads <= MAX_BLOCKS && B * max_new * q_heads <= MAX_BLOCKS;
+// The division of an attention's work (max_new <= T), or false if it is too large: its query rows, and the
+// pairs of a row tile and a cache head that its sequences can have, are below the limit of a launch's
+// blocks.  Rows are counted once, not as if every sequence had max_new of them.  The first three
+// tests keep the plan's own products in 64 bits.
+bool plan_of(int64_t B, int64_t T, int64_t max_new, int64_t max_kv, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+             w4a8::AttentionPlan& p) {
+    const int64_t rows = B * max_new < T ? B * max_new : T, widest = (max_new * (q_heads / kv_heads) + 127) / 128;
+    if (B > MAX_BLOCKS || rows * q_heads > MAX_BLOCKS || B * kv_heads * widest > MAX_BLOCKS) return false;
+    p = w4a8::attention_plan(B, max_new, max_kv, q_heads, kv_heads, head_dim);
+    return p.blocks <= MAX_BLOCKS && B * kv_heads * p.tiles <= MAX_BLOCKS;
 }
 
 }  // namespace
@@ -209,9 +216,9 @@ int64_t kv8_attention_workspace(int64_t B, int64_t T, int64_t max_new, int64_t m
         q_heads % kv_heads != 0 || q_heads > MAX_HEADS || (head_dim != 64 && head_dim != 128))
         return 0;
     max_new = bounded_new(T, max_new);
-    if (B == 0 || max_new == 0 || !fits(B, max_new, q_heads)) return 0;
-    return w4a8::attention_workspace(w4a8::attention_plan(B, max_new, max_kv, q_heads, kv_heads, head_dim), head_dim) *
-           (int64_t)sizeof(float);
+    w4a8::AttentionPlan p;
+    if (B == 0 || max_new == 0 || !plan_of(B, T, max_new, max_kv, q_heads, kv_heads, head_dim, p)) return 0;
+    return w4a8::attention_workspace(p, head_dim) * (int64_t)sizeof(float);
 }
 
 int kv8_attention(const void* q, int32_t q_heads, int64_t q_stride, const w4a8_kv8* cache, const int32_t* kv_len,
@@ -236,9 +243,8 @@ int kv8_attention(const void* q, int32_t q_heads, int64_t q_stride, const w4a8_k
     if (need > 0 && (!workspace || workspace_bytes < need)) return W4A8_ERR_INVALID_ARG;
     max_new = bounded_new(T, max_new);
     if (B == 0 || max_new == 0) return W4A8_OK;
-    if (!fits(B, max_new, q_heads) ||
-        w4a8::attention_plan(B, max_new, max_kv, q_heads, cache->heads, cache->head_dim).blocks > MAX_BLOCKS)
-        return W4A8_ERR_SHAPE;
+    w4a8::AttentionPlan p;
+    if (!plan_of(B, T, max_new, max_kv, q_heads, cache->heads, cache->head_dim, p)) return W4A8_ERR_SHAPE;
     return launched(w4a8::launch_attention(q, q_heads, q_stride, *cache, kv_len, q_start, B, T, max_new, max_kv, scale,
                                            causal, window, out, out_stride, lse, static_cast<float*>(workspace),
                                            static_cast<hipStream_t>(stream)));

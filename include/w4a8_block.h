@@ -16,6 +16,7 @@
  *     and row offsets that lie in device memory cannot be seen by the host: the kernels
  *     bound them themselves (stated at each entry), so none of them can reach memory
  *     outside the buffers described by the arguments.
+ *   - A call that would take 2^24 blocks or more is refused with W4A8_ERR_SHAPE.
  *   - Return value: W4A8_OK (0) or one of the W4A8_ERR_* codes of w4a8.h.
  *   - Dense tensors are row-major.  Activation tensors [T, heads, head_dim] have dense
  *     heads and a token stride in elements, so the queries, keys and values of one
@@ -202,6 +203,9 @@ int kv8_append(const w4a8_kv8* cache, const int32_t* ctx_len, const int32_t* q_s
  *   lse          out  NULL, or float [T, q_heads]
  *   workspace         kv8_attention_workspace(...) bytes at least (NULL if that is 0)
  * A page number outside 0..pages - 1 hides its tokens.
+ * Refused with W4A8_ERR_SHAPE: 2^24 query rows or more, min(T, B * max_new) * q_heads, or as many
+ * row tiles, B * heads * ceil(max_new * (q_heads / heads) / r), with r = 16 for less than 64
+ * rows of a sequence and cache head and 128 for more.
  */
 int kv8_attention(const void* q, int32_t q_heads, int64_t q_stride, const w4a8_kv8* cache, const int32_t* kv_len,
                   const int32_t* q_start, int64_t B, int64_t T, int64_t max_new, int64_t max_kv, float scale,

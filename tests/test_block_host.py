@@ -193,3 +193,16 @@ def test_binding_rejects_cpu_tensors():
         B.kv8_append(cache, i[None], i, torch.zeros(2, dtype=torch.int32), 1, x.view(8, 1, 64), x.view(8, 1, 64))
     with pytest.raises(ValueError):
         B.kv8_attention(x.view(8, 1, 64), cache, i[None], i, torch.zeros(2, dtype=torch.int32), 1, 1)
+
+
+def test_attention_counts_the_rows_that_exist():
+    """Sizes are bounded by the rows of a batch, not by max_new rows for every sequence."""
+    many = dict(B=16384, T=16400, max_new=15, max_kv=60000)      # one sequence of 15 tokens, the others of one
+    assert B.kv8_attention_workspace(*many.values(), 128, 32, 64) > 0
+    c = cache_desc(heads=32)
+    wide = dict(qh=128, qs=8192, os=8192)
+    assert attend(cache=c, **many, **wide) == INVALID            # only its workspace is missing
+    assert attend(cache=c, **(many | dict(T=1 << 17, max_new=1 << 17)), **wide) == SHAPE     # 2^24 rows
+    assert attend(cache=c, **(many | dict(B=1 << 18, T=1 << 13, max_new=60)), **wide) == SHAPE   # 2^24 pairs with a head
+    assert attend(cache=c, **(many | dict(B=1 << 30, T=1 << 30, max_new=1 << 30)), **wide) == SHAPE
+    assert B.kv8_attention_workspace(1 << 30, 1 << 30, 1 << 30, 1 << 30, 128, 32, 64) == 0
