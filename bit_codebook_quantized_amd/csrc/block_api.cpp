@@ -77,8 +77,8 @@ int check_rope(const w4a8_rope* r, int64_t T, int32_t head_dim) {
     return W4A8_OK;
 }
 
-int check_cache(const w4a8_kv8* c) {
-    if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !c->table) return W4A8_ERR_INVALID_ARG;
+int check_cache(const w4a8_kv8* c, int64_t B) {
+    if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || (B != 0 && !c->table)) return W4A8_ERR_INVALID_ARG;
     if (c->heads < 1 || c->pages < 1 || c->table_stride < 1) return W4A8_ERR_INVALID_ARG;
     if (c->heads > MAX_HEADS || c->pages > INT32_MAX) return W4A8_ERR_SHAPE;
     if (c->head_dim != 64 && c->head_dim != 128) return W4A8_ERR_UNSUPPORTED;
@@ -182,7 +182,7 @@ int kv8_append(const w4a8_kv8* cache, const int32_t* ctx_len, const int32_t* q_s
                int64_t max_new, const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* q,
                int32_t q_heads, int64_t q_stride, const w4a8_rope* rope, void* q_out, int64_t out_stride,
                void* stream) {
-    int st = check_cache(cache);
+    int st = check_cache(cache, B);
     if (st) return st;
     if ((st = check_batch(B, T, max_new))) return st;
     if ((st = check_heads(cache->heads, cache->head_dim, k_stride))) return st;
@@ -225,7 +225,7 @@ int kv8_attention(const void* q, int32_t q_heads, int64_t q_stride, const w4a8_k
                   const int32_t* q_start, int64_t B, int64_t T, int64_t max_new, int64_t max_kv, float scale,
                   int32_t causal, int64_t window, void* out, int64_t out_stride, float* lse, void* workspace,
                   int64_t workspace_bytes, void* stream) {
-    int st = check_cache(cache);
+    int st = check_cache(cache, B);
     if (st) return st;
     if ((st = check_batch(B, T, max_new))) return st;
     if (max_kv < 0 || window < 0 || (causal != 0 && causal != 1) || !(scale > 0.0f) || !isfinite(scale))

@@ -142,7 +142,7 @@ typedef struct w4a8_kv8 {
     int32_t head_dim;          /* 64 or 128 */
     int32_t page_tokens;       /* 16, 32, 64 or 128 */
     int32_t table_stride;      /* >= 1, pages of a table row */
-    const int32_t* table;      /* device [B, table_stride] */
+    const int32_t* table;      /* device [B, table_stride]; may be NULL if B is 0 */
 } w4a8_kv8;
 
 /*

@@ -206,3 +206,10 @@ def test_attention_counts_the_rows_that_exist():
     assert attend(cache=c, **(many | dict(B=1 << 18, T=1 << 13, max_new=60)), **wide) == SHAPE   # 2^24 pairs with a head
     assert attend(cache=c, **(many | dict(B=1 << 30, T=1 << 30, max_new=1 << 30)), **wide) == SHAPE
     assert B.kv8_attention_workspace(1 << 30, 1 << 30, 1 << 30, 1 << 30, 128, 32, 64) == 0
+
+
+def test_batches_of_no_sequences():
+    """An empty table has no address."""
+    c = cache_desc(table=None)
+    assert attend(cache=c, B=0, kv=None, start=None) == OK and attend(cache=c) == INVALID
+    assert append(at=c, B=0, T=0, ctx=None, start=None, k=None, v=None) == OK and append(at=c) == INVALID
