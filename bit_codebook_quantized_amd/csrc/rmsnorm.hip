@@ -28,8 +28,8 @@ __device__ __forceinline__ Place place_of(int slot, int nb) {
 // Bound by memory: x and the residual are read once, h and the int8 rows written once (7 bytes an
 // element with a bf16 stream), two barriers a row (sum of squares, maximum).  2048 x 4096 bf16:
 // 13.9 us, 4.2 TB/s where a large copy reaches 4.9; 1237 x 12288 fp32: 42.6 us, 3.9 TB/s; one row
-// of 4096: 3.7 us, which is latency.  Occupancy hides the barriers: 8 blocks of a 4096-column row
-// share a CU.
+// of 4096: 3.7 us, which is latency.  Occupancy hides the barriers: 7 blocks of a 4096-column row
+// share a CU (20,992 bytes of LDS each).
 // RES: the stream's type (uint16_t = bf16 bits, float), HAS_RES: whether there is a
 // residual at all.
 template <typename RES, bool HAS_RES>

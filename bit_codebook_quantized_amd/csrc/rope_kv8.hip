@@ -79,7 +79,7 @@ __device__ __forceinline__ void turn_in_piece(float (&lo)[8], float (&hi)[8], in
 }
 
 constexpr int ROPE_THREADS = 256;
-constexpr int ROPE_LDS_PAIRS = 512;    // cos/sin entries of a block: tokens a block times pairs
+constexpr int ROPE_LDS_PAIRS = ROPE_THREADS;    // cos/sin entries of a block: tokens a block times pairs
 
 struct RopeRun {    // one tensor to rotate
     const uint16_t* x;
@@ -394,7 +394,7 @@ RopeArgs rope_args(const w4a8_rope* r, bool inverse) {
     return a;
 }
 
-// Tokens a block so that every thread makes at most two cosines, heads split until a small
+// Tokens a block so that every thread makes at most one cosine, heads split until a small
 // batch gives two blocks a CU.
 RopeRun rope_run(const void* x, void* out, int64_t T, int heads, int head_dim, int64_t x_stride, int64_t out_stride,
                  int pairs) {
@@ -403,6 +403,7 @@ RopeRun rope_run(const void* x, void* out, int64_t T, int heads, int head_dim, i
     a.out = static_cast<uint16_t*>(out);
     a.T = T; a.x_stride = x_stride; a.out_stride = out_stride;
     a.heads = heads; a.head_dim = head_dim;
+    static_assert(W4A8_ROPE_MAX_HEAD_DIM / 2 <= ROPE_LDS_PAIRS && 8 * 16 <= ROPE_LDS_PAIRS, "a block's cosines fit");
     a.tokens_per_block = std::max(1, std::min(8, ROPE_THREADS / std::max(pairs, 16)));
     const int64_t tb = (T + a.tokens_per_block - 1) / a.tokens_per_block;
     a.heads_per_block = heads;
