@@ -548,9 +548,10 @@ __device__ __forceinline__ bool own_item(const AttArgs& a, Piece& p, Item& x) {
 // values of a tile while its scores are made, the keys of the next one while its weights are
 // used.  The W waves take the step's W tiles and are joined through LDS.
 // Bound by memory where the cache is long: 16 sequences of 2 k to 32 k tokens, 8 cache heads of
-// 128: 109 us and 5 for the join, 5.0 TB/s of codes; loading the values a step ahead as well
-// was 3 % slower.  By latency where it is short: 1000 tokens of one sequence 11.6 us, 300 tokens
-// 7.7 us.
+// 128: 109 us and 6 for the join, 4.9 TB/s of codes (with lse and without; a window of 1024: 21 us);
+// loading the values a step ahead as well was 3 % slower.  By latency where it is short: 1000 tokens of
+// one sequence 11.5 us, 300 tokens 7.9 us.  5 tokens each over up to 8 k: 51 us, over a window
+// of 1024 28 us.
 template <int D, bool ONE_PAGE, bool DEAL, int W>
 __global__ __launch_bounds__(64 * W, 2) void kv8_attention_kernel(AttArgs a) {
     constexpr int NK = D / 64;       // 16-byte key loads a lane and sub-tile
@@ -847,12 +848,16 @@ __device__ __forceinline__ int lds_piece(int r, int p) {
 // 16 g + 8 e .. + 7 of a value column are its piece 4 e + g.  Two blocks share a CU and are not
 // in step, so one's matrix work meets the other's vector work (one block of 256 rows, whose
 // waves pass the barrier together, was 5 % faster on 4096 of 16384 tokens and 15 to 30 %
-// slower on prompts of 2000).  With 128 rows the loop is near three limits at once, matrix
-// instructions, LDS reads and vector instructions (about 2100, 2300 and 2800 cycles a tile and
-// CU); reads are issued four ahead of the products that use them, which the compiler does not do
-// itself.  4096 of 16384 tokens, 32 heads of 128: 991 us, 971 TFLOP/s.  With 64 rows it is bound
-// by one step's chain of latencies, barrier to barrier: with HALVES = 2 waves 4 to 7 take every
-// second tile, beside the others, and the two results are added in LDS at the end.
+// slower on prompts of 2000).  Reads are issued four ahead of the products that use them, which
+// the compiler does not do itself.  With 128 rows (4096 of 16384 tokens, 32 heads of 128: 993 us, 969
+// TFLOP/s) a wave issues 380 vector instructions a tile, 68 of them matrix products: by the counters
+// vector issue takes 65 % of a SIMD's time and the matrix units 42 %, LDS reads 40 % of a CU's (a
+// quarter of that bank conflicts); matrix and vector work overlap, but do not hide each other.  With 64
+// rows (prompts of 2000 and 125, 16 heads of 64) it is 15 other vector instructions for each matrix one:
+// vector issue takes 78 %, matrix units 18 %, and the last causal rows are the longest chain of
+// steps: with HALVES = 2 waves 4 to 7 take every second tile, beside the others, and the two results are
+// added in LDS at the end.  2048 of 2048 tokens 66 to 70 us with lse and without, a window of 1024 50,
+// not causal 84.
 template <int D, bool ONE_PAGE, bool SPLIT, bool LSE, int P_QT, int HALVES = 1>
 __global__ __launch_bounds__(64 * P_WAVES * HALVES, 2) void kv8_prompt_kernel(AttArgs a) {
     static_assert(HALVES == 1 || (HALVES == 2 && !SPLIT && P_QT == 1), "halves of a whole context");
@@ -1109,7 +1114,7 @@ using Size = std::integral_constant<int, N>;
 
 }  // namespace
 
-// Blocks of a launch.
+// Blocks of a launch.  Times of two sides are of one build each; the present one is within 3 % of them.
 // Few rows, short contexts, few of them: a block of 8 waves for each pair, no parts (1 x 1000
 // tokens, 8 cache heads: 11.3 us against 11.9 and a launch more; 1 x 2048: 16.4 against 12.5;
 // 16 x up to 2048: 17.7 against 20.8; 16 x up to 4096: 28.1 against 27.5).

@@ -27,8 +27,10 @@ __device__ __forceinline__ Place place_of(int slot, int nb) {
 
 // Bound by memory: x and the residual are read once, h and the int8 rows written once (7 bytes an
 // element with a bf16 stream), two barriers a row (sum of squares, maximum).  2048 x 4096 bf16:
-// 13.9 us, 4.2 TB/s where a large copy reaches 4.9; 1237 x 12288 fp32: 42.6 us, 3.9 TB/s; one row
-// of 4096: 3.7 us, which is latency.  Occupancy hides the barriers: 7 blocks of a 4096-column row
+// 14.1 us, 4.2 TB/s where a large copy reaches 4.9; 1237 x 12288 fp32: 42.4 us, 3.9 TB/s; one row
+// of 4096: 3.8 us, which is latency.  2048 x 4096 without a residual 10.5 us (3 bytes an element, 2.4
+// TB/s: the rotation and its barrier no longer hide), bf16 rows alone 8.6 us (3.9 TB/s), with a residual 13.8
+// us (4.9 TB/s).  Occupancy hides the barriers: 7 blocks of a 4096-column row
 // share a CU (20,992 bytes of LDS each).
 // RES: the stream's type (uint16_t = bf16 bits, float), HAS_RES: whether there is a
 // residual at all.
@@ -100,7 +102,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_quant_kernel(const uint16_t* __r
 // the sum of its rows' dweight in registers; the partial rows, one a block, are added by the next
 // kernel in a fixed order (no atomics: the same bits every time).
 // Bound by memory: 14 bytes an element with an fp32 stream.  8192 x 4096 fp32: 95 us and 5 for
-// dweight, 4.7 TB/s; 4096 x 4096 bf16: 35 us, 3.8 TB/s; 8192 x 512 bf16: 15 us.  The weight's
+// dweight, 4.7 TB/s; 4096 x 4096 bf16: 35 us, 3.8 TB/s; 8192 x 512 bf16: 15 us; 2048 x 4096 bf16
+// without grad_h 21.7 us, and without the rotation as well 20.9 us.  The weight's
 // columns and the dweight sums hold 32 registers, so four waves share a SIMD.
 template <typename RES, bool ROT, bool HAS_GH>
 __global__ __launch_bounds__(1024) void rmsnorm_grad_kernel(const uint16_t* __restrict__ grad,

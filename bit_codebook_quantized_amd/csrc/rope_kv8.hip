@@ -91,7 +91,7 @@ struct RopeRun {    // one tensor to rotate
 
 // tokens_per_block tokens and heads_per_block heads a block: the cosines and sines are made
 // once a block, one pair a thread, and used for all its heads.  Bound by memory: 3001 tokens of
-// 40 x 128: 12.1 us, 5.1 TB/s; 1024 of 20 x 64: 3.6 us, a launch's latency.
+// 40 x 128: 12.2 us, 5.0 TB/s; 1024 of 20 x 64: 3.7 us, a launch's latency.
 __device__ void rope_block(const RopeRun& a, const RopeArgs& r, int64_t block, float* cosv, float* sinv) {
     const int64_t t0 = block / a.head_blocks * a.tokens_per_block;
     const int h0 = (int)(block % a.head_blocks) * a.heads_per_block;
@@ -356,9 +356,10 @@ __device__ void append_values(const AppendArgs& a, const PageJob& job, int head,
 // Blocks below cache_blocks each own one page of one sequence, one head, and its keys or its
 // values, so nothing is shared between blocks (no atomics); the rest rotate the queries.
 // 16 single tokens, 32 + 8 heads of 128: 5.6 us, the chain of dependent loads (lengths, page
-// number, old scale); 3265 tokens of three prompts: 21 to 22 us, 3.4 TB/s, where the queries
-// alone take 11 and the pages alone 16, which is the pages' latency again (the rotation is
-// 1 us of it; 512 threads a block changed nothing).
+// number, then, after the maximum, the old scale); 3265 tokens of three prompts: 21 us, 3.5 TB/s,
+// where the queries alone take 11 and the pages alone 16 (512 threads a block changed nothing): by the
+// counters vector issue takes 72 % of the time that a CU is busy and LDS 18 %, two thirds of it
+// bank conflicts of the value codes' byte stores.
 template <int NI>
 __global__ __launch_bounds__(ROPE_THREADS) void kv8_append_kernel(AppendArgs a, RopeArgs r, RopeRun q) {
     __shared__ __attribute__((aligned(16))) uint8_t vt[128 * VT_STRIDE];

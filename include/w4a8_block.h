@@ -187,17 +187,21 @@ int kv8_append(const w4a8_kv8* cache, const int32_t* ctx_len, const int32_t* q_s
  * queries: scores are exact products summed in fp32; the weights, relative to the largest
  * seen so far (as is the value scale), are rounded to fp16 (11 bits; below 2^-29 of the
  * largest in steps of 2^-39) for the product with the values, which sums in fp32.  The
- * sum of the weights is in fp32 and independent of value scales: of the weights as rounded
- * where fp16 holds them to 11 bits (that rounding then nearly cancels), else unrounded.
- * out is rounded once to bf16.  A masked key or value never reaches the result, whatever it holds.
+ * sum of the weights, in fp32, has no part in that scale: it is of the weights as rounded (the
+ * rounding then nearly cancels), or unrounded where a small value scale leaves fp16 too few bits.
+ * out is rounded once to bf16.  A masked key or value never reaches the result, whatever it
+ * holds; a page of NaN scales that a row sees makes the row NaN.
  *
  *   q            in   bf16 bits, T tokens of q_heads heads, q_stride elements apart
  *   q_heads           multiple of cache->heads
  *   kv_len       in   int32 [B], cached tokens (the new ones among them); bounded by the
  *                     table row's capacity
  *   q_start      in   int32 [B + 1], ascending, bounded by T
- *   max_new           upper bound of n; further rows of a sequence are not computed
- *   max_kv            upper bound of kv_len, used for the division of work only
+ *   max_new           upper bound of n; further rows of a sequence are not computed (rows of q that
+ *                     are not computed leave out and lse as they are)
+ *   max_kv            upper bound of kv_len, used for the division of work only.  It and max_new
+ *                     divide the whole call: single tokens over long contexts beside a
+ *                     prompt run undivided, and are much faster in a call of their own
  *   scale             > 0, finite
  *   out          out  bf16 bits [T, q_heads, head_dim], out_stride apart
  *   lse          out  NULL, or float [T, q_heads]
