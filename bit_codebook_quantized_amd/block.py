@@ -128,8 +128,6 @@ def _heads(x: torch.Tensor, name: str, heads: Optional[int] = None, head_dim: Op
     return stride[0] if t > 1 else h * d
 
 
-
-
 def _norm(m, k, x, weight, residual, eps, qmax, h, rstd, y, xq, xs):
     _is(weight, (k,), torch.float32, "weight")
     stream = torch.bfloat16
@@ -323,7 +321,9 @@ def kv8_attention(q, cache: KVCache8, table, kv_len, q_start, max_new: int, max_
     kv_len[b] cached tokens (the new ones among them): bf16 [T, q_heads, head_dim].  scale
     defaults to head_dim ** -0.5; ``window`` > 0 keeps the last window tokens of each
     position.  ``lse`` float32 [T, q_heads] is written if given.  max_new and max_kv bound
-    the new and the cached tokens of a sequence.  ``workspace``: a uint8 tensor of
+    the new and the cached tokens of a sequence, and divide the work of the whole call: single
+    tokens over long contexts are much faster in a call without prompts.  Rows of q that belong
+    to no sequence, or lie past its max_new, are not written.  ``workspace``: a uint8 tensor of
     kv8_attention_workspace(...) bytes at least, allocated if None."""
     batch = kv_len.numel()
     desc = cache.desc(table, batch)
